@@ -67,8 +67,11 @@ typedef struct CUstream_st* pararnn_stream_t;
 
 /* element type of u */
 enum { PARARNN_F32 = 0, PARARNN_BF16 = 1 };
-/* cell selector */
-enum { PARARNN_GRU = 0, PARARNN_LSTM = 1 };
+/* cell selector: the nonlinear cells, and the cells of the gated linear
+ * recurrence (pararnn_linrec_*) */
+enum { PARARNN_GRU = 0, PARARNN_LSTM = 1, PARARNN_LIN_GRU = 2, PARARNN_LIN_DECAY = 3 };
+/* gate activation of pararnn_block_norm */
+enum { PARARNN_ACT_SILU = 0, PARARNN_ACT_SIGMOID = 1 };
 
 /* host return codes */
 #define PARARNN_OK 0
@@ -476,6 +479,116 @@ int pararnn_lstm_step(const void* u_t, int u_dtype, const float* a,
                       const float* bias, const float* c_prev,
                       const float* h_prev, float* c_next, float* h_next,
                       int B, int D, pararnn_stream_t stream);
+
+/* ------------------------------------------ gated linear recurrence --
+ * Cells whose gates read the projections only, never the state: one scan in
+ * place of the Newton iterations.  (The pages have no counterpart; these
+ * stand beside the nonlinear cells, for layers that mix the two.)
+ *   PARARNN_LIN_GRU, G = 2, gates (z, c): the ParaGRU cell with a = 0,
+ *     z = sig(u_z + b_z)   c = tanh(u_c + b_c)   h_t = (1 - z) h_{t-1} + z c
+ *   PARARNN_LIN_DECAY, G = 3, gates (r, i, x), a decay per channel:
+ *     r = sig(u_r + b_r)   i = sig(u_i + b_i)   x = u_x + b_x
+ *     log a = -kappa softplus(lam) r
+ *     h_t = a h_{t-1} + sqrt(1 - a^2) i x
+ * Layouts as above, with G as here, and
+ *   lam    [D]     fp32, PARARNN_LIN_DECAY only (NULL for PARARNN_LIN_GRU)
+ *   bias   [G][D]  fp32 or NULL (zeros)
+ *   reset  [B][T]  bytes or NULL: where nonzero, the state that enters the
+ *                  step is zero, whatever it was (infinities and NaN too):
+ *                  the first step of a document packed into the row.
+ * u may be a part of a larger projection: element (b, t, q, d) lies at
+ * u[b * u_stride_b + t * u_stride_t + q * u_stride_g + d].  The strides are
+ * multiples of 8 elements and >= 0, u is 16-byte aligned.
+ * kappa > 0 and finite (ignored for PARARNN_LIN_GRU).
+ * The states are fp32 throughout.  Results do not depend on timing: equal
+ * calls return equal bits.  Outputs must not overlap inputs, but for
+ * h_next == h_prev of the step. */
+int pararnn_linrec_solve(int cell, const void* u, int u_dtype,
+                         long long u_stride_b, long long u_stride_t,
+                         long long u_stride_g, const float* lam,
+                         const float* bias, const float* h0,
+                         const unsigned char* reset, float* h, int B, int T,
+                         int D, float kappa, pararnn_stream_t stream);
+
+/* Bytes of workspace pararnn_linrec_adjoint needs (0 on invalid sizes).  It
+ * needs no initialisation and keeps nothing from call to call; calls that
+ * overlap on the GPU need one each. */
+size_t pararnn_linrec_workspace_size(int cell, int B, int T, int D);
+
+/* Adjoint of pararnn_linrec_solve along its states h: with lambda_t = dL/dh_t
+ * in total, lambda_t = dLdh_t + a_{t+1} lambda_{t+1} (no second term across a
+ * reset),
+ *   du   = dL/du                  [B][T][G][D] contiguous, du_dtype fp32 or,
+ *                                 for bf16 u, bf16
+ *   dlam = dL/dlam (NULL to skip; NULL for PARARNN_LIN_GRU)   [D]
+ *   dbias= sum_{b,t} du before its rounding (NULL to skip)    [G][D]
+ *   dh0  = dL/dh0 (NULL to skip)                              [B][D]
+ * The sums over (b, t) are reduced in a fixed order. */
+int pararnn_linrec_adjoint(int cell, const void* u, int u_dtype,
+                           long long u_stride_b, long long u_stride_t,
+                           long long u_stride_g, const float* lam,
+                           const float* bias, const float* h0,
+                           const unsigned char* reset, const float* h,
+                           const float* dLdh, void* du, int du_dtype,
+                           float* dlam, float* dbias, float* dh0, int B,
+                           int T, int D, float kappa, void* workspace,
+                           size_t ws_bytes, pararnn_stream_t stream);
+
+/* One decode step: u_t (b, q, d) at u_t[b * u_stride_b + q * u_stride_g + d],
+ * h_prev [B][D] or NULL (zeros), h_next [B][D] (may be h_prev). */
+int pararnn_linrec_step(int cell, const void* u_t, int u_dtype,
+                        long long u_stride_b, long long u_stride_g,
+                        const float* lam, const float* bias,
+                        const float* h_prev, float* h_next, int B, int D,
+                        float kappa, pararnn_stream_t stream);
+
+/* ------------------------------------------------------- block norm --
+ * The norms around a recurrent block fused with its gate and its residual
+ * scale: what stands between the states of one layer (fp32, from the solves)
+ * and the projection of the next.  Per row of D channels, each part optional:
+ *   n = h / sqrt(mean(h^2) + eps) * w_post     (w_post NULL: n = h)
+ *   y = n * act(gate)                          (gate NULL: y = n)
+ *   s = res + scale * y                        (res NULL: 0, scale NULL: 1)
+ *   x = s / sqrt(mean(s^2) + eps) * w_pre      (w_pre NULL: no x)
+ * act: PARARNN_ACT_SILU (g sig(g)) or PARARNN_ACT_SIGMOID.
+ * h, gate, res: [N] rows of D channels, fp32 or bf16 each, with a row stride
+ * in elements (a multiple of 8, >= 0).  w_post, scale, w_pre: [D] fp32.
+ * s (NULL to skip when x is wanted) and x: [N][D] contiguous, fp32 or bf16
+ * each.  Arithmetic is fp32 and each output is rounded once: x is the norm of
+ * the sum before it is rounded to s's type.
+ * s may be res itself (same type, row stride D); otherwise outputs must not
+ * overlap inputs.  Requirements: N >= 1; D % 8 == 0, D <= 8192; eps > 0;
+ * every pointer 16-byte aligned. */
+int pararnn_block_norm(const void* h, int h_dtype, long long h_stride,
+                       const void* gate, int gate_dtype, long long gate_stride,
+                       int act, const float* w_post, const void* res,
+                       int res_dtype, long long res_stride, const float* scale,
+                       const float* w_pre, void* s, int s_dtype, void* x,
+                       int x_dtype, float eps, long long N, int D,
+                       pararnn_stream_t stream);
+
+/* Bytes of workspace pararnn_block_norm_adjoint needs (0 on invalid sizes);
+ * no initialisation, one per call that may overlap another. */
+size_t pararnn_block_norm_workspace_size(long long N, int D);
+
+/* Adjoint of pararnn_block_norm: from ds = dL/ds (NULL: zero) and dx = dL/dx
+ * (given exactly when w_pre is),
+ *   dh, dgate, dres           [N][D] contiguous, in the types of h, gate, res
+ *                             (dgate NULL exactly when gate is; dres NULL to
+ *                             skip, and when res is NULL)
+ *   dw_post, dscale, dw_pre   [D] fp32 sums over the rows in a fixed order
+ *                             (NULL to skip, and when the part is absent).
+ * The parts of the chain are recomputed from h, gate and res: these must hold
+ * what the forward call read (res before an in-place update). */
+int pararnn_block_norm_adjoint(
+    const void* h, int h_dtype, long long h_stride, const void* gate,
+    int gate_dtype, long long gate_stride, int act, const float* w_post,
+    const void* res, int res_dtype, long long res_stride, const float* scale,
+    const float* w_pre, const void* ds, int ds_dtype, long long ds_stride,
+    const void* dx, int dx_dtype, long long dx_stride, void* dh, void* dgate,
+    void* dres, float* dw_post, float* dscale, float* dw_pre, float eps,
+    long long N, int D, void* workspace, size_t ws_bytes,
+    pararnn_stream_t stream);
 
 /* Human-readable text for a return code. */
 const char* pararnn_strerror(int code);

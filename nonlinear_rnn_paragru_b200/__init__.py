@@ -10,8 +10,11 @@ kernels; there is no CPU fallback.  If the shared library has not been built
 
 Convenience wrappers (:func:`gru_solve`, :func:`lstm_solve`, :func:`adjoint`)
 allocate outputs, stats and workspace with torch and call the same entry
-points.
+points.  Beside the nonlinear solves stand the gated linear recurrence
+(:func:`linrec_solve`, :func:`linrec_adjoint`, :func:`linrec_step`) and the
+norms around a block (:func:`block_norm`, :func:`block_norm_adjoint`).
 """
+import contextlib
 import ctypes
 import os
 
@@ -30,11 +33,18 @@ __all__ = [
     "pararnn_shard_apply",
     "pararnn_strerror", "gru_solve", "lstm_solve", "adjoint", "seq_baseline",
     "gru_step", "lstm_step",
+    "PARARNN_LIN_GRU", "PARARNN_LIN_DECAY", "PARARNN_ACT_SILU", "PARARNN_ACT_SIGMOID",
+    "pararnn_linrec_solve", "pararnn_linrec_workspace_size", "pararnn_linrec_adjoint",
+    "pararnn_linrec_step", "linrec_solve", "linrec_adjoint", "linrec_step",
+    "pararnn_block_norm", "pararnn_block_norm_workspace_size", "pararnn_block_norm_adjoint",
+    "block_norm", "block_norm_adjoint",
     "Workspace", "read_stats",
 ]
 
 PARARNN_F32, PARARNN_BF16 = 0, 1
 PARARNN_GRU, PARARNN_LSTM = 0, 1
+PARARNN_LIN_GRU, PARARNN_LIN_DECAY = 2, 3
+PARARNN_ACT_SILU, PARARNN_ACT_SIGMOID = 0, 1
 PARARNN_FLAG_INJECT_WITHHOLD = 1
 PARARNN_FLAG_FORCE_CHUNKED = 2
 PARARNN_FLAG_FORCE_ROW = 4
@@ -77,6 +87,7 @@ def load_library():
     lib = ctypes.CDLL(path)
     vp, fp, ip = ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p
     i, sz = ctypes.c_int, ctypes.c_size_t
+    ll, fl = ctypes.c_longlong, ctypes.c_float
     op = ctypes.POINTER(PararnnOpts)
     sigs = {
         "pararnn_workspace_size": (sz, [i, i, i, i, i, i]),
@@ -107,6 +118,16 @@ def load_library():
         "pararnn_shard_apply": (i, [i, fp, fp, fp, i, i, i, vp, sz, vp]),
         "pararnn_gru_step": (i, [vp, i, fp, fp, fp, fp, i, i, vp]),
         "pararnn_lstm_step": (i, [vp, i, fp, fp, fp, fp, fp, fp, i, i, vp]),
+        "pararnn_linrec_solve": (i, [i, vp, i, ll, ll, ll, fp, fp, fp, vp, fp, i, i, i, fl, vp]),
+        "pararnn_linrec_workspace_size": (sz, [i, i, i, i]),
+        "pararnn_linrec_adjoint": (i, [i, vp, i, ll, ll, ll, fp, fp, fp, vp, fp, fp, vp, i, fp, fp,
+                                       fp, i, i, i, fl, vp, sz, vp]),
+        "pararnn_linrec_step": (i, [i, vp, i, ll, ll, fp, fp, fp, fp, i, i, fl, vp]),
+        "pararnn_block_norm": (i, [vp, i, ll, vp, i, ll, i, fp, vp, i, ll, fp, fp, vp, i, vp, i, fl,
+                                   ll, i, vp]),
+        "pararnn_block_norm_workspace_size": (sz, [ll, i]),
+        "pararnn_block_norm_adjoint": (i, [vp, i, ll, vp, i, ll, i, fp, vp, i, ll, fp, fp, vp, i, ll,
+                                           vp, i, ll, vp, vp, vp, fp, fp, fp, fl, ll, i, vp, sz, vp]),
         "pararnn_strerror": (ctypes.c_char_p, [i]),
     }
     for name, (res, args) in sigs.items():
@@ -474,3 +495,301 @@ def seq_baseline(cell, u, a, bias=None, c0=None, h0=None, stream=None):
     c = torch.empty((B, T, D), dtype=torch.float32, device=u.device) if cell == PARARNN_LSTM else None
     pararnn_seq_baseline(cell, u, a, bias, c0, h0, c, h, stream)
     return c, h
+
+
+# ------------------------------------- gated linear recurrence, block norm --
+# These calls check every shape, type and device, since the library sees
+# pointers only; they run on the device of their tensors, whatever the current
+# one is, and allocate what they return (and their scratch) on the stream they
+# launch on, so both live as long as the work in flight, in a captured graph
+# too.  Inputs made on another stream are the caller's to order, as with every
+# CUDA call.
+_DTYPES = {torch.float32: PARARNN_F32, torch.bfloat16: PARARNN_BF16}
+_LIN_CELLS = {PARARNN_LIN_GRU: 2, PARARNN_LIN_DECAY: 3}
+_ACTS = {"silu": PARARNN_ACT_SILU, "sigmoid": PARARNN_ACT_SIGMOID}
+
+
+def _code(t):
+    """The library's code of a tensor's type (-1 lets the library reject it)."""
+    return 0 if t is None else _DTYPES.get(t.dtype, -1)
+
+
+def _need(t, name, shape, device, dtypes=(torch.float32,)):
+    """Pointer of a contiguous tensor of this shape, one of these types, on
+    this device (None -> NULL)."""
+    if t is None:
+        return None
+    if t.device != device:
+        raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    return t.data_ptr()
+
+
+def _first(t, name):
+    """The device of the leading tensor of a call."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name}: pararnn expects a CUDA tensor")
+    return t.device
+
+
+@contextlib.contextmanager
+def _moved(device, stream):
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream of {stream.device} for tensors on {device}")
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        yield
+
+
+_HERE_NOW = contextlib.nullcontext()
+
+
+def _on(device, stream):
+    """The context a call launches and allocates in."""
+    if stream is None and device.index == torch.cuda.current_device():
+        return _HERE_NOW
+    return _moved(device, stream)
+
+
+def _lin_u(cell, u, ndim):
+    G = _LIN_CELLS.get(cell)
+    if G is None:
+        raise PararnnError(-1, f"linear recurrence: unknown cell {cell}")
+    dev = _first(u, "u")
+    if u.dim() != ndim or u.shape[-2] != G:
+        raise ValueError(f"u: expected {'[B, T, G, D]' if ndim == 4 else '[B, G, D]'} with G = {G},"
+                         f" got {tuple(u.shape)}")
+    if u.stride(-1) != 1 and u.shape[-1] > 1:
+        raise ValueError("u: channels must be contiguous")
+    return dev, G
+
+
+def _lin_strides(u):
+    """(batch, [step,] gate) strides in elements; an axis of one has none."""
+    return [0 if n == 1 else s for n, s in zip(u.shape[:-1], u.stride()[:-1])]
+
+
+def pararnn_linrec_solve(cell, u, lam, bias, h0, reset, h, kappa=8.0, stream=None):
+    B, T, G, D = u.shape
+    _check(load_library().pararnn_linrec_solve(
+        cell, u.data_ptr(), _code(u), *_lin_strides(u), _ptr(lam), _ptr(bias), _ptr(h0),
+        _ptr(reset, None), _ptr(h), B, T, D, kappa, _stream(stream)), "pararnn_linrec_solve")
+
+
+def pararnn_linrec_workspace_size(cell, B, T, D) -> int:
+    return int(load_library().pararnn_linrec_workspace_size(cell, B, T, D))
+
+
+def pararnn_linrec_adjoint(cell, u, lam, bias, h0, reset, h, dLdh, du, dlam, dbias, dh0,
+                           workspace, kappa=8.0, stream=None):
+    B, T, G, D = u.shape
+    _check(load_library().pararnn_linrec_adjoint(
+        cell, u.data_ptr(), _code(u), *_lin_strides(u), _ptr(lam), _ptr(bias), _ptr(h0),
+        _ptr(reset, None), _ptr(h), _ptr(dLdh), _ptr(du, None), _code(du), _ptr(dlam),
+        _ptr(dbias), _ptr(dh0), B, T, D, kappa, _wptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream)),
+        "pararnn_linrec_adjoint")
+
+
+def pararnn_linrec_step(cell, u_t, lam, bias, h_prev, h_next, kappa=8.0, stream=None):
+    B, G, D = u_t.shape
+    _check(load_library().pararnn_linrec_step(
+        cell, u_t.data_ptr(), _code(u_t), *_lin_strides(u_t), _ptr(lam), _ptr(bias),
+        _ptr(h_prev), _ptr(h_next), B, D, kappa, _stream(stream)), "pararnn_linrec_step")
+
+
+_MASKS = (torch.bool, torch.uint8)
+
+
+def _lin_params(cell, dev, B, G, D, lam, bias, h0, h0_name="h0"):
+    if (lam is None) != (cell == PARARNN_LIN_GRU):
+        raise ValueError("lam: given exactly for PARARNN_LIN_DECAY")
+    _need(lam, "lam", (D,), dev)
+    _need(bias, "bias", (G, D), dev)
+    _need(h0, h0_name, (B, D), dev)
+
+
+def linrec_solve(cell, u, lam=None, bias=None, h0=None, *, reset=None, kappa=8.0, out=None,
+                 stream=None):
+    """Gated linear recurrence: u [B, T, G, D] (bf16 or fp32) -> states h
+    [B, T, D] fp32.  cell PARARNN_LIN_GRU (G = 2: z, c) or PARARNN_LIN_DECAY
+    (G = 3: r, i, x, with lam [D]).  u may be a view into a larger projection
+    (channels contiguous, strides multiples of 8 elements, 16-byte aligned).
+    reset [B, T] (bool or uint8): the state that enters a marked step is zero.
+    `out`: the tensor to write h to."""
+    dev, G = _lin_u(cell, u, 4)
+    B, T, _, D = u.shape
+    _lin_params(cell, dev, B, G, D, lam, bias, h0)
+    _need(reset, "reset", (B, T), dev, _MASKS)
+    _need(out, "out", (B, T, D), dev)
+    with _on(dev, stream):
+        h = torch.empty((B, T, D), dtype=torch.float32, device=dev) if out is None else out
+        pararnn_linrec_solve(cell, u, lam, bias, h0, reset, h, kappa)
+    return h
+
+
+def linrec_adjoint(cell, u, lam, bias, h0, h, dLdh, *, reset=None, kappa=8.0, want_params=True,
+                   want_dh0=True, du_dtype=None, out=None, stream=None):
+    """Adjoint of :func:`linrec_solve` along its states h: a dict of du
+    [B, T, G, D] (u's type, or `du_dtype` = torch.float32), dlam [D], dbias
+    [G, D] and dh0 [B, D] (None where not wanted or absent).  `out`: a dict of
+    tensors to write to instead of new ones."""
+    dev, G = _lin_u(cell, u, 4)
+    B, T, _, D = u.shape
+    _lin_params(cell, dev, B, G, D, lam, bias, h0)
+    _need(reset, "reset", (B, T), dev, _MASKS)
+    if h is None or dLdh is None:
+        raise ValueError("h and dLdh are needed")
+    _need(h, "h", (B, T, D), dev)
+    _need(dLdh, "dLdh", (B, T, D), dev)
+    o = out or {}
+    _need(o.get("du"), "du", u.shape, dev, (torch.float32, torch.bfloat16))
+    with _on(dev, stream):
+        def new(name, shape, dtype=torch.float32):
+            t = o.get(name)
+            if t is None:
+                return torch.empty(shape, dtype=dtype, device=dev)
+            if name != "du":
+                _need(t, name, shape, dev)
+            return t
+        du = new("du", (B, T, G, D), du_dtype or u.dtype)
+        dlam = new("dlam", (D,)) if want_params and cell == PARARNN_LIN_DECAY else None
+        dbias = new("dbias", (G, D)) if want_params else None
+        dh0 = new("dh0", (B, D)) if want_dh0 else None
+        ws = torch.empty(max(256, pararnn_linrec_workspace_size(cell, B, T, D)), dtype=torch.uint8,
+                         device=dev)
+        pararnn_linrec_adjoint(cell, u, lam, bias, h0, reset, h, dLdh, du, dlam, dbias, dh0, ws,
+                               kappa)
+    return {"du": du, "dlam": dlam, "dbias": dbias, "dh0": dh0}
+
+
+def linrec_step(cell, u_t, lam=None, bias=None, h_prev=None, *, kappa=8.0, out=None, stream=None):
+    """One decode step of the gated linear recurrence: u_t [B, G, D] -> the
+    next state [B, D].  `out` may be `h_prev` (in-place update)."""
+    dev, G = _lin_u(cell, u_t, 3)
+    B, _, D = u_t.shape
+    _lin_params(cell, dev, B, G, D, lam, bias, h_prev, "h_prev")
+    _need(out, "out", (B, D), dev)
+    with _on(dev, stream):
+        h = torch.empty((B, D), dtype=torch.float32, device=dev) if out is None else out
+        pararnn_linrec_step(cell, u_t, lam, bias, h_prev, h, kappa)
+    return h
+
+
+def pararnn_block_norm(h, h_stride, gate, gate_stride, act, w_post, res, res_stride, scale, w_pre, s,
+                       x, eps, N, D, stream=None):
+    _check(load_library().pararnn_block_norm(
+        h.data_ptr(), _code(h), h_stride, None if gate is None else gate.data_ptr(), _code(gate),
+        gate_stride, act, _ptr(w_post), None if res is None else res.data_ptr(), _code(res),
+        res_stride, _ptr(scale), _ptr(w_pre), _ptr(s, None), _code(s), _ptr(x, None), _code(x), eps,
+        N, D, _stream(stream)), "pararnn_block_norm")
+
+
+def pararnn_block_norm_workspace_size(N, D) -> int:
+    return int(load_library().pararnn_block_norm_workspace_size(N, D))
+
+
+def pararnn_block_norm_adjoint(h, h_stride, gate, gate_stride, act, w_post, res, res_stride, scale,
+                               w_pre, ds, ds_stride, dx, dx_stride, dh, dgate, dres, dw_post, dscale,
+                               dw_pre, eps, N, D, workspace, stream=None):
+    _check(load_library().pararnn_block_norm_adjoint(
+        h.data_ptr(), _code(h), h_stride, None if gate is None else gate.data_ptr(), _code(gate),
+        gate_stride, act, _ptr(w_post), None if res is None else res.data_ptr(), _code(res),
+        res_stride, _ptr(scale), _ptr(w_pre), None if ds is None else ds.data_ptr(), _code(ds),
+        ds_stride, None if dx is None else dx.data_ptr(), _code(dx), dx_stride, _ptr(dh, None),
+        _ptr(dgate, None), _ptr(dres, None), _ptr(dw_post), _ptr(dscale), _ptr(dw_pre), eps, N, D,
+        _wptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)),
+        "pararnn_block_norm_adjoint")
+
+
+def _rows(t, name, shape, dev):
+    """Row stride in elements of a [..., D] tensor whose leading axes make up
+    one axis of rows (0 for None)."""
+    if t is None:
+        return 0
+    if t.device != dev or t.shape != shape:
+        raise ValueError(f"{name}: expected {tuple(shape)} on {dev}, got {tuple(t.shape)} on {t.device}")
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] > 1:
+        raise ValueError(f"{name}: channels must be contiguous")
+    ld, rows = None, 1          # rows below the axis at hand, and their common stride
+    for n, s in zip(reversed(shape[:-1]), reversed(st[:-1])):
+        if n == 1:
+            continue
+        if ld is None:
+            ld = s
+        elif s != ld * rows:
+            raise ValueError(f"{name}: rows must lie at one stride")
+        rows *= n
+    return shape[-1] if ld is None else ld
+
+
+def _norm_parts(h, gate, act, w_post, res, scale, w_pre):
+    dev = _first(h, "h")
+    shape = h.shape
+    if h.dim() < 1 or h.numel() == 0:
+        raise PararnnError(-1, f"block norm of shape {tuple(shape)}")
+    if act not in _ACTS:
+        raise ValueError(f"act: expected one of {sorted(_ACTS)}, got {act!r}")
+    D = shape[-1]
+    for t, name in ((w_post, "w_post"), (scale, "scale"), (w_pre, "w_pre")):
+        _need(t, name, (D,), dev)
+    return (dev, shape, h.numel() // D, D, _rows(h, "h", shape, dev), _rows(gate, "gate", shape, dev),
+            _rows(res, "res", shape, dev))
+
+
+def block_norm(h, *, gate=None, act="silu", w_post=None, res=None, scale=None, w_pre=None, eps=1e-6,
+               s_dtype=None, x_dtype=torch.bfloat16, want_s=True, out=None, stream=None):
+    """The norms around a block with its gate and residual scale, on the rows
+    of h [..., D] (fp32 states or a bf16 projection), each part optional:
+
+        s = res + scale * (rms_norm(h) * w_post) * act(gate)
+        x = rms_norm(s) * w_pre
+
+    Returns (s, x); x is None without w_pre, s is None with want_s=False.
+    s_dtype: res's type by default, bf16 without res.  gate, res: h's shape,
+    bf16 or fp32; they and h may be views whose rows lie at one stride (a
+    multiple of 8 elements).  `out` = (s, x), either None for a new tensor; s
+    may be res (in-place update)."""
+    dev, shape, N, D, lh, lg, lr = _norm_parts(h, gate, act, w_post, res, scale, w_pre)
+    s, x = out or (None, None)
+    _need(s, "s", shape, dev, (torch.float32, torch.bfloat16))
+    _need(x, "x", shape, dev, (torch.float32, torch.bfloat16))
+    with _on(dev, stream):
+        if s is None and (want_s or w_pre is None):
+            s = torch.empty(shape, device=dev, dtype=s_dtype or (torch.bfloat16 if res is None
+                                                                 else res.dtype))
+        if x is None and w_pre is not None:
+            x = torch.empty(shape, dtype=x_dtype, device=dev)
+        pararnn_block_norm(h, lh, gate, lg, _ACTS[act], w_post, res, lr, scale, w_pre, s, x, eps, N, D)
+    return s, x
+
+
+def block_norm_adjoint(h, ds, dx, *, gate=None, act="silu", w_post=None, res=None, scale=None,
+                       w_pre=None, eps=1e-6, stream=None):
+    """Adjoint of :func:`block_norm` from ds = dL/ds (or None) and dx = dL/dx
+    (given exactly when w_pre is): a dict of dh, dgate, dres (contiguous, in
+    the types of h, gate, res) and dw_post, dscale, dw_pre [D] fp32, None
+    where the part is absent.  h, gate and res hold what the forward call
+    read."""
+    dev, shape, N, D, lh, lg, lr = _norm_parts(h, gate, act, w_post, res, scale, w_pre)
+    if (dx is None) != (w_pre is None):
+        raise ValueError("dx: given exactly when w_pre is")
+    lds, ldx = _rows(ds, "ds", shape, dev), _rows(dx, "dx", shape, dev)
+    with _on(dev, stream):
+        def like(t):
+            return None if t is None else torch.empty(shape, dtype=t.dtype, device=dev)
+        def sums(t):
+            return None if t is None else torch.empty((D,), dtype=torch.float32, device=dev)
+        dh, dg, dr = like(h), like(gate), like(res)
+        dwp, dsc, dwq = sums(w_post), sums(scale), sums(w_pre)
+        ws = torch.empty(max(256, pararnn_block_norm_workspace_size(N, D)), dtype=torch.uint8, device=dev)
+        pararnn_block_norm_adjoint(h, lh, gate, lg, _ACTS[act], w_post, res, lr, scale, w_pre, ds, lds,
+                                   dx, ldx, dh, dg, dr, dwp, dsc, dwq, eps, N, D, ws)
+    return {"dh": dh, "dgate": dg, "dres": dr, "dw_post": dwp, "dscale": dsc, "dw_pre": dwq}

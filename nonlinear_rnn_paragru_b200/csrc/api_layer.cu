@@ -7,7 +7,7 @@
 #include "linrec_cell.cuh"
 
 namespace pararnn {
-long long linrec_ctas(int B, int T, int D);
+long long linrec_most_ctas(int B, int D);
 size_t linrec_part_floats(int cell, int B, int T, int D);
 int launch_linrec_fwd(int cell, bool bf16, LinParams p, cudaStream_t stream);
 int launch_linrec_bwd(int cell, bool bf16, bool bf16_out, LinParams p, float* dlam, float* dbias,
@@ -109,7 +109,7 @@ int pararnn_linrec_solve(int cell, const void* u, int u_dtype, long long u_strid
   const int rc = lin_args(cell, u, u_dtype, u_stride_b, u_stride_t, u_stride_g, lam, bias, B, T, D, kappa);
   if (rc) return rc;
   if (!h) return PARARNN_ERR_INVALID_ARG;
-  if (linrec_ctas(B, T, D) >= (1LL << 31)) return PARARNN_ERR_TOO_LARGE;
+  if (linrec_most_ctas(B, D) >= (1LL << 31)) return PARARNN_ERR_TOO_LARGE;
   if (!aligned(h, 16) || (h0 && !aligned(h0, 4))) return PARARNN_ERR_MISALIGNED;
   LinParams p = lin_params(u, u_stride_b, u_stride_t, u_stride_g, lam, bias, h0, reset, B, T, D, kappa);
   p.h = h;
@@ -132,7 +132,7 @@ int pararnn_linrec_adjoint(int cell, const void* u, int u_dtype, long long u_str
   if (!h || !dLdh || !du || !workspace || (cell == PARARNN_LIN_GRU && dlam)) return PARARNN_ERR_INVALID_ARG;
   if (!is_dtype(du_dtype) || (du_dtype == PARARNN_BF16 && u_dtype != PARARNN_BF16))
     return PARARNN_ERR_UNSUPPORTED_DTYPE;
-  if (linrec_ctas(B, T, D) >= (1LL << 31)) return PARARNN_ERR_TOO_LARGE;
+  if (linrec_most_ctas(B, D) >= (1LL << 31)) return PARARNN_ERR_TOO_LARGE;
   if (!aligned(h, 16) || !aligned(dLdh, 16) || !aligned(du, 16) || (h0 && !aligned(h0, 4)) ||
       (dlam && !aligned(dlam, 4)) || (dbias && !aligned(dbias, 4)) || (dh0 && !aligned(dh0, 4)) ||
       !aligned(workspace, 256))

@@ -26,14 +26,11 @@ __device__ __forceinline__ Raw8 raw_load(const void* p, long long i, bool f32) {
   if (f32) r.b = q[1];
   return r;
 }
-__device__ __forceinline__ float2 bf2(unsigned v) {
-  return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
-}
 __device__ __forceinline__ void raw_get(const Raw8& r, bool f32, float (&v)[8]) {
   const unsigned w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 t = bf2(w[i]);
+    const float2 t = bf16_pair(w[i]);
     v[2 * i] = f32 ? __uint_as_float(w[2 * i]) : t.x;
     v[2 * i + 1] = f32 ? __uint_as_float(w[2 * i + 1]) : t.y;
   }
@@ -61,7 +58,7 @@ __device__ __forceinline__ void vec8(const float* w, int c, float (&v)[8]) {
 
 // sig(g) and its complement
 __device__ __forceinline__ void sig2(float g, float& q, float& qc) {
-  const float t = exp_neg_abs(g), pos = rcp(1.f + t), neg = t * pos;
+  const float t = ex2(-kLog2e * fabsf(g)), pos = rcp(1.f + t), neg = t * pos;
   q = g >= 0.f ? pos : neg;
   qc = g >= 0.f ? neg : pos;
 }

@@ -2,15 +2,19 @@
 // sequence), adjoint (one reverse scan) and the single decode step.
 //
 // Layout of the scans.  A cluster of CL CTAs owns a 64-channel tile of one
-// batch row and walks its sequence in rounds of CL x 8 x k steps: CTA r, warp
-// w, takes k <= kLinSteps consecutive steps, lane l the channels 2l and 2l + 1.
-// In a round a thread forms its steps' coefficients and their composed map
-// (P, Q) in registers; the 8 warps' maps meet in shared memory, the CTAs' maps
-// in each other's shared memory (one cluster barrier a round, two buffers in
-// turn), and every thread composes what precedes its own steps and runs them
-// again from the true state.  The state that enters a round is kept in a
-// register of every warp.  So u is read once, h written once, and nothing
-// waits on global memory: no workspace, no flags, no order of blocks.
+// batch row and walks its sequence in rounds of CL x W x K steps (the adjoint
+// from the last step to the first): CTA r, warp w, takes K consecutive steps,
+// lane l the channels 2l and 2l + 1.  In a round a thread composes its steps'
+// map (P, Q); the W warps' maps meet in shared memory, the CTAs' maps in each
+// other's shared memory (one cluster barrier a round, two buffers in turn),
+// and every thread composes what precedes its own steps and runs them again
+// from the true state.  The state that enters a round stays in a register of
+// every warp.  So each input is read once, each output written once, and
+// nothing waits on global memory: no workspace, no flags, no order of blocks.
+//
+// Every warp copies its own rows into a ring of S rounds in shared memory
+// (16-byte cp.async, S - 1 rounds ahead), which keeps HBM busy through the
+// rounds' barriers without holding registers.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -22,279 +26,333 @@ namespace cg = cooperative_groups;
 namespace pararnn {
 namespace {
 
-constexpr int kLinThreads = 256;
-constexpr int kLinWarps = kLinThreads / 32;
-constexpr int kLinSteps = 8;      // steps of a thread in one round
-constexpr int kLinTile = 64;      // channels of a tile
+constexpr int kLinTile = 64;  // channels of a tile
 constexpr int kLinMaxCluster = 8;
 
-// The maps of a round: per warp, and per CTA of the cluster.
-struct LinShared {
-  float4 warp[2][kLinWarps][32];
-  float4 cta[2][kLinMaxCluster][32];
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// One kind of row in a warp's ring: 64 channels of kBytes each, 16 bytes a
+// lane, so an instruction moves kRows rows.
+template <int kBytes>
+struct Rows {
+  static constexpr int kRow = 64 * kBytes;       // bytes of a row
+  static constexpr int kLanes = kRow / 16;       // lanes of a row
+  static constexpr int kRows = 32 / kLanes;
+  static constexpr int kPiece = 16 / kBytes;     // channels of a lane
 };
 
-__device__ __forceinline__ void lin_then4(float4& a, const float4& b) {
-  lin_then(a.x, a.y, b.x, b.y);
-  lin_then(a.z, a.w, b.z, b.w);
-}
+// The maps of a round: per warp, and per CTA of the cluster.
+template <int W>
+struct LinShared {
+  float4 warp[2][W][32];
+  float4 cta[2][kLinMaxCluster][32];
+};
 
 // Publish the warp's map and return the state that enters this thread's steps;
 // `carry` is the state that enters the round, and becomes the one that leaves
 // it.  Positions (wpos of the warp, rpos of the CTA) run in the order of the
 // scan.
-__device__ __forceinline__ float2 lin_exchange(LinShared& sh, int par, float4 mine, int wpos, int rpos,
-                                               int CL, int lane, float2& carry) {
+template <int W, bool kReset>
+__device__ __forceinline__ float2 lin_exchange(LinShared<W>& sh, int par, float4 mine, int wpos, int rpos, int CL,
+                                               int lane, float2& carry) {
   sh.warp[par][wpos][lane] = mine;
   __syncthreads();
+  float2 in = carry;
   if (CL > 1) {
     cg::cluster_group cl = cg::this_cluster();
-    if (wpos < CL) {  // warp position w tells CTA position w
-      float4 all = sh.warp[par][0][lane];
+    float4 all = sh.warp[par][0][lane], before = make_float4(1.f, 1.f, 0.f, 0.f);
 #pragma unroll
-      for (int i = 1; i < kLinWarps; ++i) lin_then4(all, sh.warp[par][i][lane]);
-      *cl.map_shared_rank(&sh.cta[par][rpos][lane], (unsigned)wpos) = all;
+    for (int i = 1; i < W; ++i) {
+      if (i == wpos) before = all;
+      all = lin_then<kReset>(all, sh.warp[par][i][lane]);
     }
+    for (int i = wpos; i < CL; i += W) *cl.map_shared_rank(&sh.cta[par][rpos][lane], (unsigned)i) = all;
     cl.sync();
-    float2 in = carry;
     for (int i = 0; i < CL; ++i) {
       if (i == rpos) in = carry;
-      const float4 v = sh.cta[par][i][lane];
-      carry.x = lin_apply(v.x, v.y, carry.x);
-      carry.y = lin_apply(v.z, v.w, carry.y);
+      carry = lin_apply<kReset>(sh.cta[par][i][lane], carry);
     }
-#pragma unroll
-    for (int i = 0; i < kLinWarps; ++i)
-      if (i < wpos) {
-        const float4 v = sh.warp[par][i][lane];
-        in.x = lin_apply(v.x, v.y, in.x);
-        in.y = lin_apply(v.z, v.w, in.y);
-      }
-    return in;
+    return wpos ? lin_apply<kReset>(before, in) : in;
   }
-  float2 in = carry;
 #pragma unroll
-  for (int i = 0; i < kLinWarps; ++i) {
+  for (int i = 0; i < W; ++i) {
     if (i == wpos) in = carry;
-    const float4 v = sh.warp[par][i][lane];
-    carry.x = lin_apply(v.x, v.y, carry.x);
-    carry.y = lin_apply(v.z, v.w, carry.y);
+    carry = lin_apply<kReset>(sh.warp[par][i][lane], carry);
   }
   return in;
 }
 
-// bit j: the state entering step t0 + j is zero
-__device__ __forceinline__ unsigned lin_resets(const unsigned char* reset, size_t row, int t0, int n,
-                                               int lane) {
-  if (!reset) return 0u;
-  const bool r = lane < n && reset[row + t0 + lane] != 0;
-  return __ballot_sync(0xffffffffu, r);
-}
+// Shape of a scan kernel: W warps, K steps of a thread in a round, a ring of S
+// rounds, at least R CTAs on an SM.
+template <int CELL, bool kBF16>
+struct FwdShape {
+  static constexpr bool kGru = CELL == PARARNN_LIN_GRU;
+  static constexpr int W = 8, K = 8, S = kBF16 ? (kGru ? 3 : 4) : (kGru ? 3 : 2), R = kBF16 && kGru ? 3 : 2;
+};
 
 template <int CELL, bool kBF16>
-__global__ void __launch_bounds__(kLinThreads) linrec_fwd(const LinParams p, const int CL) {
+struct FwdRing {
+  using U = Rows<kBF16 ? 2 : 4>;
+  static constexpr int K = FwdShape<CELL, kBF16>::K, G = LinCell<CELL>::G;
+  static constexpr int kRound = K * G * U::kRow;  // bytes of a warp's round
+  static constexpr int kWarp = FwdShape<CELL, kBF16>::S * kRound;
+  static constexpr int kBytes = FwdShape<CELL, kBF16>::W * kWarp;
+};
+
+template <bool kBF16>
+__device__ __forceinline__ float2 row_pair(const char* row, int lane) {
+  if (kBF16) return bf16_pair(*reinterpret_cast<const unsigned*>(row + 4 * lane));
+  return *reinterpret_cast<const float2*>(row + 8 * lane);
+}
+
+template <int CELL, bool kBF16, bool kReset>
+__global__ void __launch_bounds__(32 * FwdShape<CELL, kBF16>::W, FwdShape<CELL, kBF16>::R)
+    linrec_fwd(const LinParams p, const int CL) {
   using Cell = LinCell<CELL>;
-  constexpr int G = Cell::G, K = kLinSteps;
-  __shared__ LinShared sh;
+  using Shape = FwdShape<CELL, kBF16>;
+  using Ring = FwdRing<CELL, kBF16>;
+  using U = typename Ring::U;
+  constexpr int G = Cell::G, K = Shape::K, W = Shape::W, S = Shape::S, ES = kBF16 ? 2 : 4;
+  extern __shared__ __align__(16) char ring[];
+  __shared__ LinShared<W> sh;
   const int rank = CL > 1 ? (int)cg::this_cluster().block_rank() : 0;
   const int tile = blockIdx.x / CL;
   const int b = tile / p.ntd, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int d0 = (tile - b * p.ntd) * kLinTile + 2 * lane;
+  const int dbase = (tile - b * p.ntd) * kLinTile, d0 = dbase + 2 * lane;
   const bool live = d0 < p.D;
-  const int d = live ? d0 : p.D - 2;  // idle lanes read a channel pair that exists
-  Cell cx, cy;
-  cx.init(p.lam, p.bias, p.kappa, p.D, d);
-  cy.init(p.lam, p.bias, p.kappa, p.D, d + 1);
-  float2 carry = make_float2(0.f, 0.f);
-  if (p.h0) {
-    const float* q = p.h0 + (size_t)b * p.D + d;
-    carry = make_float2(q[0], q[1]);
-  }
-  const size_t row = (size_t)b * p.T;
-  const long long ub = (long long)b * p.sb + d;
-  const int k = p.steps, round = CL * kLinWarps * k;
-  if (CL > 1) cg::this_cluster().sync();  // every CTA runs before one writes into another
-  int par = 0;
-  for (int base = 0; base < p.T; base += round, par ^= 1) {
-    const int t0 = base + (rank * kLinWarps + warp) * k;
-    const int n = max(0, min(k, p.T - t0));
-    typename LinRaw<kBF16>::type raw[K][G];
+  const int d = live ? d0 : p.D - 2;  // idle lanes read parameters that exist
+  // copies: this lane's row of an instruction and its piece of the row
+  const int crow = lane / U::kLanes, cpiece = lane % U::kLanes;
+  const bool cok = dbase + cpiece * U::kPiece < p.D;
+  const char* src = static_cast<const char*>(p.u) + (b * p.sb + dbase + cpiece * U::kPiece) * ES;
+  const uint32_t dst = smem_u32(ring) + warp * Ring::kWarp + crow * G * U::kRow + cpiece * 16;
+  const char* const mine = ring + warp * Ring::kWarp;
+  const int round = CL * W * K, first = (rank * W + warp) * K;
+  auto copy = [&](int t0, int slot) {  // steps t0 .. t0 + K - 1 of this warp
 #pragma unroll
-    for (int j = 0; j < K; ++j) {
-      const long long at = ub + (long long)min(t0 + min(j, k - 1), p.T - 1) * p.st;
+    for (int i = 0; i < K; i += U::kRows) {
+      const int t = t0 + i + crow;
+      if (cok && t < p.T) {
+        const char* s = src + t * (p.st * ES);
+        const uint32_t o = dst + slot * Ring::kRound + i * G * U::kRow;
 #pragma unroll
-      for (int q = 0; q < G; ++q) raw[j][q] = lin_load<kBF16>(p.u, at + q * p.sg);
-    }
-    const unsigned resets = lin_resets(p.reset, row, t0, n, lane);
-    float4 m[K];  // (m, b) of both channels
-    float4 map = make_float4(1.f, 0.f, 1.f, 0.f);
-#pragma unroll
-    for (int j = 0; j < K; ++j) {
-      float ux[G], uy[G];
-#pragma unroll
-      for (int q = 0; q < G; ++q) {
-        const float2 v = LinRaw<kBF16>::get(raw[j][q]);
-        ux[q] = v.x;
-        uy[q] = v.y;
+        for (int q = 0; q < G; ++q) cp_async16(o + q * U::kRow, s + q * (p.sg * ES));
       }
-      float4 c;
-      cx.coef(ux, c.x, c.y);
-      cy.coef(uy, c.z, c.w);
-      if (j >= n) c = make_float4(0.f, 0.f, 0.f, 0.f);  // no step: the identity
-      const bool rs = (resets >> j) & 1u;
-      map.y = rs ? c.y : fmaf(-c.x, map.y, map.y + c.y);
-      map.w = rs ? c.w : fmaf(-c.z, map.w, map.w + c.w);
-      map.x = fmaf(-c.x, map.x, map.x);
-      map.z = fmaf(-c.z, map.z, map.z);
-      m[j] = c;
     }
-    if (resets) map.x = map.z = -1.f;
-    float2 s = lin_exchange(sh, par, map, warp, rank, CL, lane, carry);
-    float* out = p.h + (row + t0) * p.D + d;
+  };
+#pragma unroll
+  for (int s = 0; s < S - 1; ++s) {
+    copy(first + s * round, s);
+    cp_async_commit();
+  }
+  Cell cell;
+  cell.init(p.lam, p.bias, p.kappa, p.D, d);
+  float2 carry = vec2(p.h0 ? p.h0 + (size_t)b * p.D : nullptr, d);
+  const size_t row = (size_t)b * p.T;
+  if (CL > 1) cg::this_cluster().sync();  // every CTA runs before one writes into another
+  int par = 0, slot = 0;
+  for (int base = 0; base < p.T; base += round, par ^= 1) {
+    const int t0 = base + first;
+    bool mark = false;  // lane j: a reset at step t0 + j
+    if (kReset) mark = lane < K && t0 + lane < p.T && p.reset[row + t0 + lane] != 0;
+    cp_async_wait<S - 2>();
+    __syncwarp();
+    copy(t0 + (S - 1) * round, slot == 0 ? S - 1 : slot - 1);
+    cp_async_commit();
+    const unsigned resets = kReset ? __ballot_sync(0xffffffffu, mark) : 0u;
+    const char* rows = mine + slot * Ring::kRound;
+    // steps past T compute on what the ring holds there: nothing after them is
+    // stored
+    float2 nm[K], bb[K], P = both(1.f), Q = both(0.f);
 #pragma unroll
     for (int j = 0; j < K; ++j) {
-      const bool rs = (resets >> j) & 1u;
-      s.x = rs ? m[j].y : fmaf(-m[j].x, s.x, s.x + m[j].y);
-      s.y = rs ? m[j].w : fmaf(-m[j].z, s.y, s.y + m[j].w);
-      if (j < n && live) *reinterpret_cast<float2*>(out + (size_t)j * p.D) = s;
+      float2 u[G];
+#pragma unroll
+      for (int q = 0; q < G; ++q) u[q] = row_pair<kBF16>(rows + (j * G + q) * U::kRow, lane);
+      cell.coef(u, nm[j], bb[j]);
+      Q = lin_step(nm[j], bb[j], Q);
+      P = lfma(nm[j], P, P);
+      if (kReset && ((resets >> j) & 1u)) Q = bb[j];
     }
+    if (kReset && resets) P = both(-1.f);
+    float2 h = lin_exchange<W, kReset>(sh, par, make_float4(P.x, P.y, Q.x, Q.y), warp, rank, CL, lane, carry);
+    float* out = p.h + (row + t0) * p.D + d;
+    const int n = live ? p.T - t0 : 0;
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+      h = lin_step(nm[j], bb[j], h);
+      if (kReset && ((resets >> j) & 1u)) h = bb[j];
+      if (j < n) *reinterpret_cast<float2*>(out + (size_t)j * p.D) = h;
+    }
+    slot = slot + 1 == S ? 0 : slot + 1;
   }
+  cp_async_wait<0>();
 }
 
 // Reverse scan: lambda_t = g_t + mu_{t+1}, mu_t = (1 - m_t) lambda_t (0 at a
 // reset, and mu_1 = dL/dh0).  Positions run from the last step to the first.
-template <int CELL, bool kBF16, bool kBF16Out>
-__global__ void __launch_bounds__(kLinThreads) linrec_bwd(const LinParams p, const int CL) {
+template <int CELL, bool kBF16>
+struct BwdShape {
+  static constexpr bool kGru = CELL == PARARNN_LIN_GRU;
+  static constexpr int W = 8, K = 4, S = kBF16 ? (kGru ? 4 : 3) : (kGru ? 3 : 2), R = 2;
+};
+
+template <int CELL, bool kBF16>
+struct BwdRing {
+  using U = Rows<kBF16 ? 2 : 4>;
+  using F = Rows<4>;
+  static constexpr int K = BwdShape<CELL, kBF16>::K, G = LinCell<CELL>::G;
+  static constexpr int kH = K * G * U::kRow, kG = kH + K * F::kRow;  // offsets of h_{t-1}, dL/dh
+  static constexpr int kRound = kG + K * F::kRow;
+  static constexpr int kWarp = BwdShape<CELL, kBF16>::S * kRound;
+  static constexpr int kBytes = BwdShape<CELL, kBF16>::W * kWarp;
+};
+
+template <int CELL, bool kBF16, bool kBF16Out, bool kReset>
+__global__ void __launch_bounds__(32 * BwdShape<CELL, kBF16>::W, BwdShape<CELL, kBF16>::R)
+    linrec_bwd(const LinParams p, const int CL) {
   using Cell = LinCell<CELL>;
-  constexpr int G = Cell::G, K = kLinSteps;
-  __shared__ LinShared sh;
+  using Shape = BwdShape<CELL, kBF16>;
+  using Ring = BwdRing<CELL, kBF16>;
+  using U = typename Ring::U;
+  using F = typename Ring::F;
+  constexpr int G = Cell::G, K = Shape::K, W = Shape::W, S = Shape::S, ES = kBF16 ? 2 : 4;
+  extern __shared__ __align__(16) char ring[];
+  __shared__ LinShared<W> sh;
   const int rank = CL > 1 ? (int)cg::this_cluster().block_rank() : 0;
   const int tile = blockIdx.x / CL;
   const int b = tile / p.ntd, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int d0 = (tile - b * p.ntd) * kLinTile + 2 * lane;
+  const int dbase = (tile - b * p.ntd) * kLinTile, d0 = dbase + 2 * lane;
   const bool live = d0 < p.D;
   const int d = live ? d0 : p.D - 2;
-  Cell cx, cy;
-  cx.init(p.lam, p.bias, p.kappa, p.D, d);
-  cy.init(p.lam, p.bias, p.kappa, p.D, d + 1);
   const size_t row = (size_t)b * p.T;
-  const long long ub = (long long)b * p.sb + d;
-  const int k = p.steps, round = CL * kLinWarps * k;
-  float2 carry = make_float2(0.f, 0.f);
+  const int crow = lane / U::kLanes, cpiece = lane % U::kLanes;
+  const bool cok = dbase + cpiece * U::kPiece < p.D;
+  const char* src = static_cast<const char*>(p.u) + (b * p.sb + dbase + cpiece * U::kPiece) * ES;
+  const int frow = lane / F::kLanes, fpiece = lane % F::kLanes;
+  const bool fok = dbase + fpiece * F::kPiece < p.D;
+  const size_t fcol = row * p.D + dbase + fpiece * F::kPiece;
+  const uint32_t dst = smem_u32(ring) + warp * Ring::kWarp;
+  const char* const mine = ring + warp * Ring::kWarp;
+  const int round = CL * W * K, first = (rank * W + warp) * K;
+  auto copy = [&](int t1, int slot) {  // steps t1 - 1, t1 - 2, ..., t1 - K of this warp
+    const uint32_t to = dst + slot * Ring::kRound;
+#pragma unroll
+    for (int i = 0; i < K; i += U::kRows) {
+      const int t = t1 - 1 - i - crow;
+      if (cok && t >= 0) {
+        const char* s = src + t * (p.st * ES);
+        const uint32_t o = to + (i + crow) * G * U::kRow + cpiece * 16;
+#pragma unroll
+        for (int q = 0; q < G; ++q) cp_async16(o + q * U::kRow, s + q * (p.sg * ES));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < K; i += F::kRows) {
+      const int t = t1 - 1 - i - frow;
+      const uint32_t o = to + (i + frow) * F::kRow + fpiece * 16;
+      if (fok && t >= 0) cp_async16(o + Ring::kG, p.g + fcol + (size_t)t * p.D);
+      if (fok && t >= 1) cp_async16(o + Ring::kH, p.h + fcol + (size_t)(t - 1) * p.D);
+    }
+  };
+#pragma unroll
+  for (int s = 0; s < S - 1; ++s) {
+    copy(p.T - first - s * round, s);
+    cp_async_commit();
+  }
+  Cell cell;
+  cell.init(p.lam, p.bias, p.kappa, p.D, d);
+  const float2 h0 = vec2(p.h0 ? p.h0 + (size_t)b * p.D : nullptr, d);
+  float2 carry = both(0.f);
   float2 sum[G + 1];
 #pragma unroll
-  for (int q = 0; q <= G; ++q) sum[q] = make_float2(0.f, 0.f);
+  for (int q = 0; q <= G; ++q) sum[q] = both(0.f);
   if (CL > 1) cg::this_cluster().sync();
-  int par = 0;
+  int par = 0, slot = 0;
   for (int end = p.T; end > 0; end -= round, par ^= 1) {
-    // this thread's steps, last first: t1 - 1, t1 - 2, ..., t1 - n
-    const int t1 = end - (rank * kLinWarps + warp) * k;
-    const int n = max(0, min(k, t1));
-    typename LinRaw<kBF16>::type raw[K][G];
-    float2 hp[K], g[K];
+    const int t1 = end - first;
+    bool mark = false;  // lane j: a reset at step t1 - 1 - j
+    if (kReset) mark = lane < K && t1 - 1 - lane >= 0 && p.reset[row + t1 - 1 - lane] != 0;
+    cp_async_wait<S - 2>();
+    __syncwarp();
+    copy(t1 - (S - 1) * round, slot == 0 ? S - 1 : slot - 1);
+    cp_async_commit();
+    const unsigned resets = kReset ? __ballot_sync(0xffffffffu, mark) : 0u;
+    const char* rows = mine + slot * Ring::kRound;
+    float2 nm[K], P = both(1.f), Q = both(0.f);
 #pragma unroll
     for (int j = 0; j < K; ++j) {
-      const int t = max(t1 - 1 - min(j, k - 1), 0);
-      const long long at = ub + (long long)t * p.st;
+      float2 u[G];
 #pragma unroll
-      for (int q = 0; q < G; ++q) raw[j][q] = lin_load<kBF16>(p.u, at + q * p.sg);
-      g[j] = __ldg(reinterpret_cast<const float2*>(p.g + (row + t) * p.D + d));
-      if (t > 0)
-        hp[j] = __ldg(reinterpret_cast<const float2*>(p.h + (row + t - 1) * p.D + d));
-      else if (p.h0)
-        hp[j] = make_float2(p.h0[(size_t)b * p.D + d], p.h0[(size_t)b * p.D + d + 1]);
-      else
-        hp[j] = make_float2(0.f, 0.f);
+      for (int q = 0; q < G; ++q) u[q] = row_pair<kBF16>(rows + (j * G + q) * U::kRow, lane);
+      nm[j] = cell.nm(u);
+      const float2 lt = ladd(row_pair<false>(rows + Ring::kG + j * F::kRow, lane), Q);
+      Q = lfma(nm[j], lt, lt);
+      P = lfma(nm[j], P, P);
+      if (kReset && ((resets >> j) & 1u)) Q = both(0.f);
     }
-    unsigned resets = 0u;  // bit j: step t1 - 1 - j
-    if (p.reset)
-      resets = __ballot_sync(0xffffffffu, lane < n && p.reset[row + t1 - 1 - min(lane, n - 1)] != 0);
-    float2 m[K];
-    float4 map = make_float4(1.f, 0.f, 1.f, 0.f);
-#pragma unroll
-    for (int j = 0; j < K; ++j) {
-      float ux[G], uy[G];
-#pragma unroll
-      for (int q = 0; q < G; ++q) {
-        const float2 v = LinRaw<kBF16>::get(raw[j][q]);
-        ux[q] = v.x;
-        uy[q] = v.y;
-      }
-      m[j] = make_float2(cx.forget(ux), cy.forget(uy));
-      if (j >= n) m[j] = g[j] = make_float2(0.f, 0.f);
-      const bool rs = (resets >> j) & 1u;
-      const float lx = g[j].x + map.y, ly = g[j].y + map.w;
-      map.y = rs ? 0.f : fmaf(-m[j].x, lx, lx);
-      map.w = rs ? 0.f : fmaf(-m[j].y, ly, ly);
-      map.x = fmaf(-m[j].x, map.x, map.x);
-      map.z = fmaf(-m[j].y, map.z, map.z);
-    }
-    if (resets) map.x = map.z = -1.f;
-    float2 mu = lin_exchange(sh, par, map, warp, rank, CL, lane, carry);
+    if (kReset && resets) P = both(-1.f);
+    float2 mu = lin_exchange<W, kReset>(sh, par, make_float4(P.x, P.y, Q.x, Q.y), warp, rank, CL, lane, carry);
     float2 add[G + 1];
 #pragma unroll
-    for (int q = 0; q <= G; ++q) add[q] = make_float2(0.f, 0.f);
+    for (int q = 0; q <= G; ++q) add[q] = both(0.f);
 #pragma unroll
     for (int j = 0; j < K; ++j) {
-      const bool rs = (resets >> j) & 1u;
-      const float lx = g[j].x + mu.x, ly = g[j].y + mu.y;
-      mu.x = rs ? 0.f : fmaf(-m[j].x, lx, lx);
-      mu.y = rs ? 0.f : fmaf(-m[j].y, ly, ly);
-      float ux[G], uy[G], dx[G], dy[G], ex, ey;
+      const int t = t1 - 1 - j;
+      if (t < 0) break;  // a warp's steps before the sequence: all that follow too
+      const bool rs = kReset && ((resets >> j) & 1u);
+      const float2 lt = ladd(row_pair<false>(rows + Ring::kG + j * F::kRow, lane), mu);
+      mu = rs ? both(0.f) : lfma(nm[j], lt, lt);
+      float2 hp = t == 0 ? h0 : row_pair<false>(rows + Ring::kH + j * F::kRow, lane);
+      if (rs) hp = both(0.f);
+      float2 u[G], du[G], e;
+#pragma unroll
+      for (int q = 0; q < G; ++q) u[q] = row_pair<kBF16>(rows + (j * G + q) * U::kRow, lane);
+      cell.grad(u, nm[j], hp, lt, du, e);
+      const size_t at = ((row + t) * G) * p.D + d;
 #pragma unroll
       for (int q = 0; q < G; ++q) {
-        const float2 v = LinRaw<kBF16>::get(raw[j][q]);
-        ux[q] = v.x;
-        uy[q] = v.y;
+        add[q] = ladd(add[q], du[q]);
+        if (!live) continue;
+        if constexpr (kBF16Out)
+          *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.du) + at + (size_t)q * p.D) =
+              __float22bfloat162_rn(du[q]);
+        else
+          *reinterpret_cast<float2*>(static_cast<float*>(p.du) + at + (size_t)q * p.D) = du[q];
       }
-      cx.grad(ux, rs ? 0.f : hp[j].x, lx, dx, ex);
-      cy.grad(uy, rs ? 0.f : hp[j].y, ly, dy, ey);
-      if (j < n && live) {
-        const size_t at = ((row + t1 - 1 - j) * G) * p.D + d;
-#pragma unroll
-        for (int q = 0; q < G; ++q) {
-          if constexpr (kBF16Out)
-            *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.du) + at + (size_t)q * p.D) =
-                __floats2bfloat162_rn(dx[q], dy[q]);
-          else
-            *reinterpret_cast<float2*>(static_cast<float*>(p.du) + at + (size_t)q * p.D) =
-                make_float2(dx[q], dy[q]);
-          add[q].x += dx[q];
-          add[q].y += dy[q];
-        }
-        add[G].x += ex;
-        add[G].y += ey;
+      if (CELL == PARARNN_LIN_DECAY) add[G] = ladd(add[G], e);
+      if (t == 0 && p.dh0 && live) {
+        p.dh0[(size_t)b * p.D + d] = mu.x;
+        p.dh0[(size_t)b * p.D + d + 1] = mu.y;
       }
     }
     // a round's sums first, then the running sums: over long sequences the
     // error grows with the number of rounds only
 #pragma unroll
-    for (int q = 0; q <= G; ++q) {
-      sum[q].x += add[q].x;
-      sum[q].y += add[q].y;
-    }
+    for (int q = 0; q <= G; ++q) sum[q] = ladd(sum[q], add[q]);
+    slot = slot + 1 == S ? 0 : slot + 1;
   }
-  if (p.dh0 && rank == 0 && warp == 0 && live) {
-    p.dh0[(size_t)b * p.D + d] = carry.x;
-    p.dh0[(size_t)b * p.D + d + 1] = carry.y;
-  }
+  cp_async_wait<0>();
   if (!p.part) return;
-  sum[G].x *= cx.lam_scale(p.lam, d);
-  sum[G].y *= cy.lam_scale(p.lam, d + 1);
-  // the 8 warps' sums, in warp order
+  if (CELL == PARARNN_LIN_DECAY) sum[G] = lmul(sum[G], Cell::lam_scale(p.lam, d));
+  // the warps' sums, in warp order
   __syncthreads();
-  float2* const acc = reinterpret_cast<float2*>(&sh);  // [warp][G + 1][32]
-  static_assert(sizeof(LinShared) >= kLinWarps * 4 * 32 * sizeof(float2), "sums fit");
+  float2* const acc = reinterpret_cast<float2*>(ring);  // [warp][G + 1][32]
+  static_assert(Ring::kBytes >= W * (G + 1) * 32 * (int)sizeof(float2), "sums fit");
+  static_assert(W > G, "a warp for each sum");
 #pragma unroll
   for (int q = 0; q <= G; ++q) acc[(warp * (G + 1) + q) * 32 + lane] = sum[q];
   __syncthreads();
   if (warp <= G && live) {
-    float2 s = make_float2(0.f, 0.f);
-    for (int i = 0; i < kLinWarps; ++i) {
-      const float2 v = acc[(i * (G + 1) + warp) * 32 + lane];
-      s.x += v.x;
-      s.y += v.y;
-    }
+    float2 s = both(0.f);
+    for (int i = 0; i < W; ++i) s = ladd(s, acc[(i * (G + 1) + warp) * 32 + lane]);
     float* q = p.part + ((size_t)(b * CL + rank) * (G + 1) + warp) * p.D + d;
     q[0] = s.x;
     q[1] = s.y;
@@ -332,30 +390,30 @@ __global__ void __launch_bounds__(256) linrec_step(const LinParams p, const floa
   const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
   if (i >= (long long)p.B * (p.D / 2)) return;
   const int b = (int)(i / (p.D / 2)), d = 2 * (int)(i - (long long)b * (p.D / 2));
-  float ux[G], uy[G];
+  float2 u[G];
 #pragma unroll
   for (int q = 0; q < G; ++q) {
-    const float2 v = LinRaw<kBF16>::get(lin_load<kBF16>(p.u, b * p.sb + q * p.sg + d));
-    ux[q] = v.x;
-    uy[q] = v.y;
+    const char* at = static_cast<const char*>(p.u) + (b * p.sb + q * p.sg + d) * (kBF16 ? 2 : 4);
+    u[q] = row_pair<kBF16>(at, 0);
   }
-  Cell cx, cy;
-  cx.init(p.lam, p.bias, p.kappa, p.D, d);
-  cy.init(p.lam, p.bias, p.kappa, p.D, d + 1);
-  float mx, bx, my, by;
-  cx.coef(ux, mx, bx);
-  cy.coef(uy, my, by);
+  Cell cell;
+  cell.init(p.lam, p.bias, p.kappa, p.D, d);
+  float2 nm, bb;
+  cell.coef(u, nm, bb);
   const size_t at = (size_t)b * p.D + d;
-  const float hx = h_prev ? h_prev[at] : 0.f, hy = h_prev ? h_prev[at + 1] : 0.f;
-  h_next[at] = fmaf(-mx, hx, hx + bx);
-  h_next[at + 1] = fmaf(-my, hy, hy + by);
+  const float2 h = lin_step(nm, bb, vec2(h_prev ? h_prev + (size_t)b * p.D : nullptr, d));
+  h_next[at] = h.x;
+  h_next[at + 1] = h.y;
 }
 
 template <typename Kern>
-int launch_scan(Kern kern, const LinParams& p, int CL, cudaStream_t stream) {
+int launch_scan(Kern kern, int threads, int smem, const LinParams& p, int CL, cudaStream_t stream) {
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return (int)e;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kLinThreads);
+  cfg.blockDim = dim3(threads);
   cfg.gridDim = dim3((unsigned)((long long)p.B * p.ntd * CL));
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -367,55 +425,82 @@ int launch_scan(Kern kern, const LinParams& p, int CL, cudaStream_t stream) {
   return (int)cudaLaunchKernelEx(&cfg, kern, p, CL);
 }
 
-}  // namespace
-
-// CTAs of a cluster: enough for two CTAs on each of 148 SMs, no more than the
-// sequence has 8-step pieces for.
-int linrec_cluster(int B, int T, int D) {
-  const long long tiles = (long long)B * ((D + kLinTile - 1) / kLinTile);
-  int CL = 1;
-  while (CL < kLinMaxCluster && tiles * CL < 2 * 148 && T > CL * kLinWarps * kLinSteps) CL *= 2;
-  return CL;
+template <int CELL, bool kBF16>
+int launch_fwd_t(const LinParams& p, int CL, cudaStream_t stream) {
+  constexpr int threads = 32 * FwdShape<CELL, kBF16>::W, smem = FwdRing<CELL, kBF16>::kBytes;
+  return p.reset ? launch_scan(linrec_fwd<CELL, kBF16, true>, threads, smem, p, CL, stream)
+                 : launch_scan(linrec_fwd<CELL, kBF16, false>, threads, smem, p, CL, stream);
 }
 
-long long linrec_ctas(int B, int T, int D) {
-  return (long long)B * ((D + kLinTile - 1) / kLinTile) * linrec_cluster(B, T, D);
-}
-
-size_t linrec_part_floats(int cell, int B, int T, int D) {
-  return (size_t)B * linrec_cluster(B, T, D) * (cell == PARARNN_LIN_GRU ? 3 : 4) * D;
-}
-
-static void lin_shape(LinParams& p, int CL) {
-  p.ntd = (p.D + kLinTile - 1) / kLinTile;
-  const long long lanes = (long long)CL * kLinWarps;
-  p.steps = (int)std::min<long long>(kLinSteps, (p.T + lanes - 1) / lanes);
-}
-
-int launch_linrec_fwd(int cell, bool bf16, LinParams p, cudaStream_t stream) {
-  const int CL = linrec_cluster(p.B, p.T, p.D);
-  lin_shape(p, CL);
-  if (cell == PARARNN_LIN_GRU)
-    return bf16 ? launch_scan(linrec_fwd<PARARNN_LIN_GRU, true>, p, CL, stream)
-                : launch_scan(linrec_fwd<PARARNN_LIN_GRU, false>, p, CL, stream);
-  return bf16 ? launch_scan(linrec_fwd<PARARNN_LIN_DECAY, true>, p, CL, stream)
-              : launch_scan(linrec_fwd<PARARNN_LIN_DECAY, false>, p, CL, stream);
+template <int CELL, bool kBF16, bool kBF16Out>
+int launch_bwd_t(const LinParams& p, int CL, cudaStream_t stream) {
+  constexpr int threads = 32 * BwdShape<CELL, kBF16>::W, smem = BwdRing<CELL, kBF16>::kBytes;
+  return p.reset ? launch_scan(linrec_bwd<CELL, kBF16, kBF16Out, true>, threads, smem, p, CL, stream)
+                 : launch_scan(linrec_bwd<CELL, kBF16, kBF16Out, false>, threads, smem, p, CL, stream);
 }
 
 template <int CELL>
-static int launch_bwd_t(bool bf16, bool bf16_out, const LinParams& p, int CL, cudaStream_t stream) {
-  if (!bf16) return launch_scan(linrec_bwd<CELL, false, false>, p, CL, stream);
-  return bf16_out ? launch_scan(linrec_bwd<CELL, true, true>, p, CL, stream)
-                  : launch_scan(linrec_bwd<CELL, true, false>, p, CL, stream);
+int launch_bwd_c(bool bf16, bool bf16_out, const LinParams& p, int CL, cudaStream_t stream) {
+  if (!bf16) return launch_bwd_t<CELL, false, false>(p, CL, stream);
+  return bf16_out ? launch_bwd_t<CELL, true, true>(p, CL, stream) : launch_bwd_t<CELL, true, false>(p, CL, stream);
+}
+
+// CTAs of a cluster: as many as fill one wave of `per_sm` CTAs on 148 SMs, no
+// more than the sequence has rounds of one CTA (`steps`) for.
+int cluster_for(int B, int T, int D, int per_sm, int steps) {
+  const long long tiles = (long long)B * ((D + kLinTile - 1) / kLinTile);
+  int CL = 1;
+  while (CL < kLinMaxCluster && 2 * tiles * CL <= 148 * per_sm && T > CL * steps) CL *= 2;
+  return CL;
+}
+
+template <int CELL>
+int fwd_cluster(bool bf16, int B, int T, int D) {
+  using H = FwdShape<CELL, true>;
+  using F = FwdShape<CELL, false>;
+  return bf16 ? cluster_for(B, T, D, H::R, H::W * H::K) : cluster_for(B, T, D, F::R, F::W * F::K);
+}
+
+// the same for both types of u, so that the workspace does not depend on it
+template <int CELL>
+int bwd_cluster(int B, int T, int D) {
+  using H = BwdShape<CELL, true>;
+  return cluster_for(B, T, D, H::R, H::W * H::K);
+}
+
+}  // namespace
+
+int linrec_bwd_cluster(int cell, int B, int T, int D) {
+  return cell == PARARNN_LIN_GRU ? bwd_cluster<PARARNN_LIN_GRU>(B, T, D) : bwd_cluster<PARARNN_LIN_DECAY>(B, T, D);
+}
+
+long long linrec_most_ctas(int B, int D) {
+  return (long long)B * ((D + kLinTile - 1) / kLinTile) * kLinMaxCluster;
+}
+
+size_t linrec_part_floats(int cell, int B, int T, int D) {
+  return (size_t)B * linrec_bwd_cluster(cell, B, T, D) * (cell == PARARNN_LIN_GRU ? 3 : 4) * D;
+}
+
+int launch_linrec_fwd(int cell, bool bf16, LinParams p, cudaStream_t stream) {
+  p.ntd = (p.D + kLinTile - 1) / kLinTile;
+  if (cell == PARARNN_LIN_GRU) {
+    const int CL = fwd_cluster<PARARNN_LIN_GRU>(bf16, p.B, p.T, p.D);
+    return bf16 ? launch_fwd_t<PARARNN_LIN_GRU, true>(p, CL, stream)
+                : launch_fwd_t<PARARNN_LIN_GRU, false>(p, CL, stream);
+  }
+  const int CL = fwd_cluster<PARARNN_LIN_DECAY>(bf16, p.B, p.T, p.D);
+  return bf16 ? launch_fwd_t<PARARNN_LIN_DECAY, true>(p, CL, stream)
+              : launch_fwd_t<PARARNN_LIN_DECAY, false>(p, CL, stream);
 }
 
 int launch_linrec_bwd(int cell, bool bf16, bool bf16_out, LinParams p, float* dlam, float* dbias,
                       cudaStream_t stream) {
-  const int CL = linrec_cluster(p.B, p.T, p.D);
-  lin_shape(p, CL);
+  const int CL = linrec_bwd_cluster(cell, p.B, p.T, p.D);
+  p.ntd = (p.D + kLinTile - 1) / kLinTile;
   if (!dlam && !dbias) p.part = nullptr;
-  int e = cell == PARARNN_LIN_GRU ? launch_bwd_t<PARARNN_LIN_GRU>(bf16, bf16_out, p, CL, stream)
-                                  : launch_bwd_t<PARARNN_LIN_DECAY>(bf16, bf16_out, p, CL, stream);
+  int e = cell == PARARNN_LIN_GRU ? launch_bwd_c<PARARNN_LIN_GRU>(bf16, bf16_out, p, CL, stream)
+                                  : launch_bwd_c<PARARNN_LIN_DECAY>(bf16, bf16_out, p, CL, stream);
   if (e || !p.part) return e;
   const int G = cell == PARARNN_LIN_GRU ? 2 : 3;
   const int C = (G + 1) * p.D;

@@ -1,7 +1,8 @@
 // linrec_cell.cuh -- the cells of the gated linear recurrence
 //   h_t = (1 - m_t) h_{t-1} + b_t
 // whose gates read the projections u_t only (never the state), forward and
-// adjoint, in fp32.
+// adjoint, in fp32.  A thread evaluates two neighbouring channels; sums and
+// products are packed (one instruction for both, each half rounded alone).
 //
 //   LIN_GRU    u = (z, c):     m = z = sig(u_z + b_z),  b = z tanh(u_c + b_c)
 //   LIN_DECAY  u = (r, i, x):  w = kappa softplus(lam) sig(u_r + b_r) = -log a,
@@ -9,8 +10,9 @@
 //
 // Everything is written in m = 1 - a, not in a: a decay of 0.999 rounded to
 // fp32 is off by 3e-8, which over the 1000 steps it remembers is 3e-5 of the
-// state, while m = 1e-3 is held to 2^-24 of itself and h - m h + b rounds each
-// state once.  sqrt(1 - a^2) = sqrt(m (2 - m)) has no cancellation either.
+// state, while m = 1e-3 is held to 2^-24 of itself and (h - m h) + b rounds each
+// state twice.  sqrt(1 - a^2) = sqrt(m (2 - m)) has no cancellation either.
+// The code holds nm = -m, the factor of the fma.
 #pragma once
 #include <cuda_bf16.h>
 
@@ -18,11 +20,23 @@
 
 namespace pararnn {
 
-// e^-|x|: the one exponential of a sigmoid that can neither overflow nor turn
-// an infinite argument into NaN
-__device__ __forceinline__ float exp_neg_abs(float x) { return ex2(-kLog2e * fabsf(x)); }
-
-// sqrt on the special-function unit (about 1 ulp); 0 for denormals
+// ------------------------------------------------------- packed arithmetic --
+__device__ __forceinline__ float2 lfma(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 lmul(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 ladd(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 ex2_2(float2 v) { return make_float2(ex2(v.x), ex2(v.y)); }
+// 2^-|v|: the exponential of a sigmoid that neither overflows nor turns an
+// infinite argument into NaN
+__device__ __forceinline__ float2 ex2_neg_abs(float2 v) { return make_float2(ex2(-fabsf(v.x)), ex2(-fabsf(v.y))); }
+__device__ __forceinline__ float2 rcp_2(float2 v) { return make_float2(rcp(v.x), rcp(v.y)); }
+__device__ __forceinline__ float2 neg2(float2 v) { return make_float2(-v.x, -v.y); }
+// v < 0 ? a : b, v's sign as of a gate argument times -log2 e
+__device__ __forceinline__ float2 sel_neg(float2 v, float2 a, float2 b) {
+  return make_float2(v.x < 0.f ? a.x : b.x, v.y < 0.f ? a.y : b.y);
+}
+// square root and its reciprocal on the special-function unit (about 1 ulp;
+// 0 and infinity for denormals)
 __device__ __forceinline__ float sqrt_apx(float x) {
   float y;
   asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -34,22 +48,49 @@ __device__ __forceinline__ float rsqrt_apx(float x) {
   return y;
 }
 
-// 1 - e^-w for w >= 0, to a few 2^-24 of itself for every w.  Below 1/2 the
-// Taylor series w - w^2/2! + ... - w^8/8! (the next term is below 2^-26 of the
-// sum there); above, 1 - ex2 (no cancellation: e^-w < 0.61).
-__device__ __forceinline__ float one_minus_exp(float w) {
-  float p = fmaf(w, -1.f / 40320.f, 1.f / 5040.f);
-  p = fmaf(w, p, -1.f / 720.f);
-  p = fmaf(w, p, 1.f / 120.f);
-  p = fmaf(w, p, -1.f / 24.f);
-  p = fmaf(w, p, 1.f / 6.f);
-  p = fmaf(w, p, -0.5f);
-  p = fmaf(w, p, 1.f);
-  return w < 0.5f ? w * p : 1.f - ex2(-kLog2e * w);
+constexpr float kLn2 = 0.69314718055994531f;
+
+// 2^-v - 1 = -(1 - a) for v >= 0 (v = w log2 e), to a few 2^-24 of itself.
+// Below v = 0.36 (w < 1/4) the Taylor series of -expm1 to w^6 (the next term
+// is below 2^-24 of the sum there); above, no cancellation: 2^-v < 0.78.
+__device__ __forceinline__ float2 decay_nm(float2 v) {
+  constexpr float L1 = kLn2, L2 = L1 * kLn2, L3 = L2 * kLn2, L4 = L3 * kLn2, L5 = L4 * kLn2, L6 = L5 * kLn2;
+  float2 p = lfma(v, both(L6 / 720.f), both(-L5 / 120.f));
+  p = lfma(v, p, both(L4 / 24.f));
+  p = lfma(v, p, both(-L3 / 6.f));
+  p = lfma(v, p, both(L2 / 2.f));
+  p = lfma(v, p, both(-L1));
+  p = lmul(v, p);
+  const float2 e = ladd(ex2_2(neg2(v)), both(-1.f));
+  return make_float2(v.x < 0.36f ? p.x : e.x, v.y < 0.36f ? p.y : e.y);
+}
+
+// tanh y and the parts of its derivative 1 - tanh^2 = 4 F R^2, F = e^-2|y|,
+// R = 1 / (1 + F).  Below |y| = 0.3 the Taylor series to y^9 (the next term is
+// below 2^-24 of the sum there), above (1 - F) R with F < 0.55.
+__device__ __forceinline__ float2 tanh_parts(float2 y, float2& F, float2& R) {
+  F = ex2_neg_abs(lmul(y, both(2.f * kLog2e)));
+  R = rcp_2(ladd(F, both(1.f)));
+  const float2 big = lmul(lfma(F, both(-1.f), both(1.f)), R);
+  const float2 s = lmul(y, y);
+  float2 p = lfma(s, both(62.f / 2835.f), both(-17.f / 315.f));
+  p = lfma(s, p, both(2.f / 15.f));
+  p = lfma(s, p, both(-1.f / 3.f));
+  p = lfma(s, p, both(1.f));
+  p = lmul(y, p);
+  return make_float2(fabsf(y.x) < 0.3f ? p.x : copysignf(big.x, y.x),
+                     fabsf(y.y) < 0.3f ? p.y : copysignf(big.y, y.y));
 }
 
 // log(1 + e^x), once per channel
 __device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); }
+// its logarithm's derivative sig(x) / softplus(x); 1 where e^x underflows
+__device__ __forceinline__ float dlog_softplus(float x) {
+  const float sp = softplus(x);
+  return sp > 0.f ? 1.f / (1.f + expf(-x)) / sp : 1.f;
+}
+
+__device__ __forceinline__ float2 vec2(const float* p, int d) { return p ? make_float2(p[d], p[d + 1]) : both(0.f); }
 
 template <int CELL>
 struct LinCell;
@@ -57,123 +98,115 @@ struct LinCell;
 template <>
 struct LinCell<PARARNN_LIN_GRU> {
   static constexpr int G = 2;
-  float bz, bc;
-  __device__ __forceinline__ void init(const float* /*lam*/, const float* bias, float /*kappa*/, int D,
-                                       int d) {
-    bz = bias ? bias[d] : 0.f;
-    bc = bias ? bias[D + d] : 0.f;
+  float2 bz, bc;  // -log2 e b_z, b_c
+  __device__ __forceinline__ void init(const float* /*lam*/, const float* bias, float /*kappa*/, int D, int d) {
+    bz = lmul(vec2(bias, d), both(-kLog2e));
+    bc = vec2(bias ? bias + D : nullptr, d);
   }
-  // sig(x), 1 - sig(x) and tanh(y) with one reciprocal: 1 / (1 + e^-|x|) and
-  // tanh|y| = q / (2 - q), q = 1 - e^-2|y|, over the product of denominators
-  // (at most 4)
-  __device__ __forceinline__ void gates(const float (&u)[G], float& z, float& zc, float& c) const {
-    const float x = u[0] + bz, y = u[1] + bc;
-    const float t = exp_neg_abs(x), q = one_minus_exp(2.f * fabsf(y));
-    const float d1 = 1.f + t, d2 = 2.f - q, inv = rcp(d1 * d2);
-    const float pos = d2 * inv, neg = t * pos;
-    z = x >= 0.f ? pos : neg;
-    zc = x >= 0.f ? neg : pos;
-    c = copysignf(q * d1 * inv, y);
+  __device__ __forceinline__ float2 zarg(float2 u) const { return lfma(u, both(-kLog2e), bz); }
+  // -z = 1 / -(1 + 2^v): 0 where 2^v overflows
+  __device__ __forceinline__ float2 nm(const float2 (&u)[G]) const {
+    return rcp_2(neg2(ladd(ex2_2(zarg(u[0])), both(1.f))));
   }
-  __device__ __forceinline__ void coef(const float (&u)[G], float& m, float& b) const {
-    float zc, c;
-    gates(u, m, zc, c);
-    b = m * c;
+  __device__ __forceinline__ void coef(const float2 (&u)[G], float2& m, float2& b) const {
+    float2 F, R;
+    m = nm(u);
+    b = lmul(neg2(m), tanh_parts(ladd(u[1], bc), F, R));
   }
-  __device__ __forceinline__ float forget(const float (&u)[G]) const {
-    const float x = u[0] + bz, t = exp_neg_abs(x), pos = rcp(1.f + t);
-    return x >= 0.f ? pos : t * pos;
+  // du of one step from lambda and h_{t-1}
+  __device__ __forceinline__ void grad(const float2 (&u)[G], float2 m, float2 hp, float2 lt, float2 (&du)[G],
+                                       float2& /*e*/) const {
+    float2 F, R;
+    const float2 c = tanh_parts(ladd(u[1], bc), F, R);
+    const float2 t = ex2_neg_abs(zarg(u[0])), q = rcp_2(ladd(t, both(1.f)));
+    const float2 zz = lmul(lmul(t, q), q);  // z (1 - z), exact where z is near 1 too
+    du[0] = lmul(lmul(lt, lfma(hp, both(-1.f), c)), zz);
+    du[1] = lmul(lmul(lt, m), lmul(lmul(F, both(-4.f)), lmul(R, R)));
   }
-  // du and the share of d lam for one step: hp = h_{t-1} (0 at a reset)
-  __device__ __forceinline__ void grad(const float (&u)[G], float hp, float lt, float (&du)[G],
-                                       float& e) const {
-    float z, zc, c;
-    gates(u, z, zc, c);
-    du[0] = lt * (c - hp) * (z * zc);
-    du[1] = lt * z * fmaf(-c, c, 1.f);
-    e = 0.f;
-  }
-  __device__ __forceinline__ float lam_scale(const float*, int) const { return 0.f; }
+  static __device__ __forceinline__ float2 lam_scale(const float*, int) { return both(0.f); }
 };
 
 template <>
 struct LinCell<PARARNN_LIN_DECAY> {
   static constexpr int G = 3;
-  float br, bi, bx, k;  // k = kappa softplus(lam)
+  float2 br, bi, bx, k;  // -log2 e b_r, -log2 e b_i, b_x, kappa softplus(lam) log2 e
   __device__ __forceinline__ void init(const float* lam, const float* bias, float kappa, int D, int d) {
-    br = bias ? bias[d] : 0.f;
-    bi = bias ? bias[D + d] : 0.f;
-    bx = bias ? bias[2 * D + d] : 0.f;
-    k = kappa * softplus(lam[d]);
+    br = lmul(vec2(bias, d), both(-kLog2e));
+    bi = lmul(vec2(bias ? bias + D : nullptr, d), both(-kLog2e));
+    bx = vec2(bias ? bias + 2 * (size_t)D : nullptr, d);
+    k = lmul(make_float2(softplus(lam[d]), softplus(lam[d + 1])), both(kappa * kLog2e));
   }
-  // the two sigmoids and their complements over one reciprocal
-  __device__ __forceinline__ void gates(const float (&u)[G], float& r, float& rc, float& i, float& ic) const {
-    const float x = u[0] + br, y = u[1] + bi;
-    const float tx = exp_neg_abs(x), ty = exp_neg_abs(y);
-    const float dx = 1.f + tx, dy = 1.f + ty, inv = rcp(dx * dy);
-    const float px = dy * inv, py = dx * inv, nx = tx * px, ny = ty * py;
-    r = x >= 0.f ? px : nx;
-    rc = x >= 0.f ? nx : px;
-    i = y >= 0.f ? py : ny;
-    ic = y >= 0.f ? ny : py;
+  // r, i and, over one reciprocal, t = 2^-|arg|, q = 1 / (1 + t) of each
+  __device__ __forceinline__ void gates(const float2 (&u)[G], float2& r, float2& i, float2& tr, float2& qr,
+                                        float2& ti, float2& qi, float2& vr) const {
+    vr = lfma(u[0], both(-kLog2e), br);
+    const float2 vi = lfma(u[1], both(-kLog2e), bi);
+    tr = ex2_neg_abs(vr);
+    ti = ex2_neg_abs(vi);
+    const float2 dr = ladd(tr, both(1.f)), di = ladd(ti, both(1.f)), inv = rcp_2(lmul(dr, di));
+    qr = lmul(di, inv);
+    qi = lmul(dr, inv);
+    // sig(x) is q for x >= 0 (v <= 0), t q below
+    r = lmul(sel_neg(neg2(vr), tr, both(1.f)), qr);
+    i = lmul(sel_neg(neg2(vi), ti, both(1.f)), qi);
   }
-  __device__ __forceinline__ void coef(const float (&u)[G], float& m, float& b) const {
-    float r, rc, i, ic;
-    gates(u, r, rc, i, ic);
-    m = one_minus_exp(k * r);
-    b = sqrt_apx(m * (2.f - m)) * i * (u[2] + bx);
+  __device__ __forceinline__ float2 nm(const float2 (&u)[G]) const {
+    const float2 r = rcp_2(ladd(ex2_2(lfma(u[0], both(-kLog2e), br)), both(1.f)));
+    return decay_nm(lmul(k, r));
   }
-  __device__ __forceinline__ float forget(const float (&u)[G]) const {
-    const float x = u[0] + br, t = exp_neg_abs(x), pos = rcp(1.f + t);
-    return one_minus_exp(k * (x >= 0.f ? pos : t * pos));
+  __device__ __forceinline__ void coef(const float2 (&u)[G], float2& m, float2& b) const {
+    float2 r, i, tr, qr, ti, qi, vr;
+    gates(u, r, i, tr, qr, ti, qi, vr);
+    m = decay_nm(lmul(k, r));
+    const float2 s = lmul(m, ladd(m, both(2.f)));  // -(1 - a^2)
+    b = lmul(lmul(make_float2(sqrt_apx(-s.x), sqrt_apx(-s.y)), i), ladd(u[2], bx));
   }
-  __device__ __forceinline__ void grad(const float (&u)[G], float hp, float lt, float (&du)[G],
-                                       float& e) const {
-    float r, rc, i, ic;
-    gates(u, r, rc, i, ic);
-    const float x = u[2] + bx, w = k * r, m = one_minus_exp(w), a = 1.f - m, s = m * (2.f - m);
-    const float rb = s >= 1.1754944e-38f ? rsqrt_apx(s) : 0.f;  // 1 / beta; w / beta -> 0 with w
-    const float beta = s * rb;
-    // dL/dr * r: beta' = -(a^2 / beta) (d log a), log a = -w
-    e = lt * (a * i * x * (a * (w * rb)) - a * hp * w);
-    du[0] = e * rc;
-    du[1] = lt * beta * x * (i * ic);
-    du[2] = lt * beta * i;
+  __device__ __forceinline__ void grad(const float2 (&u)[G], float2 m, float2 hp, float2 lt, float2 (&du)[G],
+                                       float2& e) const {
+    float2 r, i, tr, qr, ti, qi, vr;
+    gates(u, r, i, tr, qr, ti, qi, vr);
+    const float2 x = ladd(u[2], bx), a = ladd(m, both(1.f)), w = lmul(lmul(k, r), both(kLn2));
+    const float2 s = lmul(neg2(m), ladd(m, both(2.f)));  // beta^2
+    // 1 / beta; w / beta -> 0 with w
+    const float2 rb = make_float2(s.x >= 1.1754944e-38f ? rsqrt_apx(s.x) : 0.f,
+                                  s.y >= 1.1754944e-38f ? rsqrt_apx(s.y) : 0.f);
+    const float2 beta = lmul(s, rb);
+    // r dL/dr = lambda (a^2 i x w / beta - a h_{t-1} w):  d beta = (a^2 / beta) dw
+    const float2 ix = lmul(i, x);
+    e = lmul(lmul(lt, a), lfma(lmul(a, ix), lmul(w, rb), neg2(lmul(hp, w))));
+    du[0] = lmul(e, lmul(sel_neg(neg2(vr), both(1.f), tr), qr));
+    const float2 lb = lmul(lt, beta);
+    du[1] = lmul(lmul(lb, x), lmul(lmul(ti, qi), qi));
+    du[2] = lmul(lb, i);
   }
-  // dlam = (sum of e) sig(lam) / softplus(lam); the ratio is 1 where e^lam underflows
-  __device__ __forceinline__ float lam_scale(const float* lam, int d) const {
-    const float sp = softplus(lam[d]);
-    return sp > 0.f ? 1.f / (1.f + expf(-lam[d])) / sp : 1.f;
+  static __device__ __forceinline__ float2 lam_scale(const float* lam, int d) {
+    return make_float2(dlog_softplus(lam[d]), dlog_softplus(lam[d + 1]));
   }
 };
 
-// Affine maps h -> P h + Q of consecutive steps.  P < 0 marks a run of steps
-// with a reset in it: what came before is forgotten even where it is infinite
-// or NaN (0 * inf would carry it on).
-__device__ __forceinline__ float lin_apply(float P, float Q, float h) { return P < 0.f ? Q : fmaf(P, h, Q); }
-// (P, Q) <- the run (P, Q) followed by the run (P2, Q2)
-__device__ __forceinline__ void lin_then(float& P, float& Q, float P2, float Q2) {
-  Q = lin_apply(P2, Q2, Q);
-  P = (P < 0.f || P2 < 0.f) ? -1.f : P * P2;
+// h <- (h - m h) + b: the fma rounds (1 - m) h once, m near 1 included
+__device__ __forceinline__ float2 lin_step(float2 nm, float2 b, float2 h) { return ladd(lfma(nm, h, h), b); }
+
+// Affine maps h -> P h + Q of consecutive steps, two channels: (Px, Py, Qx, Qy).
+// With resets, P < 0 marks a run of steps with one in it: what came before is
+// forgotten even where it is infinite or NaN (0 * inf would carry it on).
+template <bool kReset>
+__device__ __forceinline__ float2 lin_apply(float4 v, float2 h) {
+  const float2 n = lfma(make_float2(v.x, v.y), h, make_float2(v.z, v.w));
+  if (!kReset) return n;
+  return v.x < 0.f ? make_float2(v.z, v.w) : n;  // a reset holds for both channels
+}
+// the run `a` followed by the run `b`
+template <bool kReset>
+__device__ __forceinline__ float4 lin_then(float4 a, float4 b) {
+  const float2 q = lin_apply<kReset>(b, make_float2(a.z, a.w));
+  float2 p = lmul(make_float2(a.x, a.y), make_float2(b.x, b.y));
+  if (kReset && (a.x < 0.f || b.x < 0.f)) p = both(-1.f);
+  return make_float4(p.x, p.y, q.x, q.y);
 }
 
-// Two neighbouring channels of u.
-template <bool kBF16>
-struct LinRaw {
-  using type = float2;
-  static __device__ __forceinline__ float2 get(type v) { return v; }
-};
-template <>
-struct LinRaw<true> {
-  using type = unsigned;
-  static __device__ __forceinline__ float2 get(type v) {
-    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
-  }
-};
-template <bool kBF16>
-__device__ __forceinline__ typename LinRaw<kBF16>::type lin_load(const void* u, long long i) {
-  const char* p = static_cast<const char*>(u) + i * (kBF16 ? 2 : 4);
-  return __ldg(reinterpret_cast<const typename LinRaw<kBF16>::type*>(p));
+__device__ __forceinline__ float2 bf16_pair(unsigned v) {
+  return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
 }
 
 struct LinParams {
@@ -191,7 +224,6 @@ struct LinParams {
   float* part;           // adjoint: [B * CL][(G + 1) D] sums over a CTA's steps
   int B, T, D;
   int ntd;               // 64-channel tiles in D
-  int steps;             // steps of a warp in one round
 };
 
 }  // namespace pararnn

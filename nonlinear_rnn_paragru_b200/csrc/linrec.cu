@@ -5,10 +5,9 @@
 // batch row and walks its sequence in rounds of CL x W x K steps (the adjoint
 // from the last step to the first): CTA r, warp w, takes K consecutive steps,
 // lane l the channels 2l and 2l + 1.  In a round a thread composes its steps'
-// map (P, Q); the W warps' maps meet in shared memory, the CTAs' maps in each
-// other's shared memory (one cluster barrier a round, two buffers in turn),
-// and every thread composes what precedes its own steps and runs them again
-// from the true state.  The state that enters a round stays in a register of
+// maps (P, Q); the W warps' maps meet in shared memory, the CTAs' maps in each
+// other's shared memory (asynchronous stores, two buffers in turn), and every
+// thread composes what precedes its own steps and applies its maps to that.  The state that enters a round stays in a register of
 // every warp.  So each input is read once, each output written once, and
 // nothing waits on global memory: no workspace, no flags, no order of blocks.
 //
@@ -48,45 +47,101 @@ struct Rows {
   static constexpr int kPiece = 16 / kBytes;     // channels of a lane
 };
 
-// The maps of a round: per warp, and per CTA of the cluster.
+// The warps' maps of a round, and the mbarriers that count the arrival of the
+// CTAs' maps; those lie in dynamic shared memory, kLinBufs x CL x 512 bytes.
+constexpr int kLinBufs = 2;
 template <int W>
 struct LinShared {
   float4 warp[2][W][32];
-  float4 cta[2][kLinMaxCluster][32];
+  uint64_t bar[kLinBufs];
 };
 
-// Publish the warp's map and return the state that enters this thread's steps;
-// `carry` is the state that enters the round, and becomes the one that leaves
-// it.  Positions (wpos of the warp, rpos of the CTA) run in the order of the
-// scan.
-template <int W, bool kReset>
-__device__ __forceinline__ float2 lin_exchange(LinShared<W>& sh, int par, float4 mine, int wpos, int rpos, int CL,
-                                               int lane, float2& carry) {
-  sh.warp[par][wpos][lane] = mine;
-  __syncthreads();
+__device__ __forceinline__ uint32_t map_rank(uint32_t addr, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+// 16 bytes into another CTA of the cluster, counted by the mbarrier there: no
+// fence, so the stores of states in flight are not waited for
+__device__ __forceinline__ void st_async16(uint32_t addr, uint32_t bar, float4 v) {
+  asm volatile(
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr),
+      "r"(__float_as_uint(v.x)), "r"(__float_as_uint(v.y)), "r"(__float_as_uint(v.z)), "r"(__float_as_uint(v.w)),
+      "r"(bar)
+      : "memory");
+}
+
+constexpr uint64_t kLinWaitNs = 2000000000ull;
+
+template <int CL, bool kReset>
+__device__ __forceinline__ float2 lin_join(const float4* cta, int rpos, int lane, float2& carry) {
+  float4 v[CL];
+#pragma unroll
+  for (int i = 0; i < CL; ++i) v[i] = cta[i * 32 + lane];
   float2 in = carry;
-  if (CL > 1) {
-    cg::cluster_group cl = cg::this_cluster();
-    float4 all = sh.warp[par][0][lane], before = make_float4(1.f, 1.f, 0.f, 0.f);
 #pragma unroll
-    for (int i = 1; i < W; ++i) {
-      if (i == wpos) before = all;
-      all = lin_then<kReset>(all, sh.warp[par][i][lane]);
-    }
-    for (int i = wpos; i < CL; i += W) *cl.map_shared_rank(&sh.cta[par][rpos][lane], (unsigned)i) = all;
-    cl.sync();
-    for (int i = 0; i < CL; ++i) {
-      if (i == rpos) in = carry;
-      carry = lin_apply<kReset>(sh.cta[par][i][lane], carry);
-    }
-    return wpos ? lin_apply<kReset>(before, in) : in;
-  }
-#pragma unroll
-  for (int i = 0; i < W; ++i) {
-    if (i == wpos) in = carry;
-    carry = lin_apply<kReset>(sh.warp[par][i][lane], carry);
+  for (int i = 0; i < CL; ++i) {
+    if (i == rpos) in = carry;
+    carry = lin_apply<kReset>(v[i], carry);
   }
   return in;
+}
+
+// Publish the warp's map of round r and return the state that enters this
+// thread's steps; `carry`, the state that enters the round, becomes the one
+// that leaves it.  Positions (wpos of the warp, rpos of the CTA) run in the
+// order of the scan.  Buffers and mbarriers alternate: a CTA can only send the
+// maps of round r + 2 after every CTA's of round r + 1 came, which each sends
+// after all its warps have read those of round r.  The wait for the cluster is
+// bounded; where it runs out the states become NaN.
+template <int W, bool kReset>
+__device__ __forceinline__ float2 lin_exchange(LinShared<W>& sh, float4* cta, unsigned r, float4 mine, int wpos,
+                                               int rpos, int CL, int lane, float2& carry, bool& lost) {
+  const int par = r & 1;
+  sh.warp[par][wpos][lane] = mine;
+  __syncthreads();
+  float4 v[W];
+#pragma unroll
+  for (int i = 0; i < W; ++i) v[i] = sh.warp[par][i][lane];
+  float2 in = carry;
+  if (CL == 1) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      if (i == wpos) in = carry;
+      carry = lin_apply<kReset>(v[i], carry);
+    }
+    return in;
+  }
+  float4 before = make_float4(1.f, 1.f, 0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < W - 1; ++i)
+    if (i < wpos) before = i ? lin_then<kReset>(before, v[i]) : v[0];
+  if (wpos == W - 1) {
+    const float4 all = lin_then<kReset>(before, mine);
+    if (lane == 0) mbar_arrive_expect_tx(&sh.bar[par], CL * 512);
+    const uint32_t at = smem_u32(&cta[(par * CL + rpos) * 32 + lane]), bar = smem_u32(&sh.bar[par]);
+    for (int i = 0; i < CL; ++i) st_async16(map_rank(at, i), map_rank(bar, i), all);
+  }
+  if (!lost) lost = !mbar_wait_bounded(&sh.bar[par], (r >> 1) & 1, kLinWaitNs);
+  const float4* maps = cta + par * CL * 32;
+  if (CL == 2)
+    in = lin_join<2, kReset>(maps, rpos, lane, carry);
+  else if (CL == 4)
+    in = lin_join<4, kReset>(maps, rpos, lane, carry);
+  else
+    in = lin_join<8, kReset>(maps, rpos, lane, carry);
+  if (lost) carry = in = both(__int_as_float(0x7fffffff));
+  return wpos ? lin_apply<kReset>(before, in) : in;
+}
+
+// Before the rounds: the mbarriers, and every CTA of the cluster runs before
+// one writes into another.
+template <int W>
+__device__ __forceinline__ void lin_cluster_start(LinShared<W>& sh, int CL) {
+  if (CL == 1) return;
+  if (threadIdx.x == 0)
+    for (int i = 0; i < kLinBufs; ++i) mbar_init(&sh.bar[i], 1);
+  cg::this_cluster().sync();
 }
 
 // Shape of a scan kernel: W warps, K steps of a thread in a round, a ring of S
@@ -94,7 +149,11 @@ __device__ __forceinline__ float2 lin_exchange(LinShared<W>& sh, int par, float4
 template <int CELL, bool kBF16>
 struct FwdShape {
   static constexpr bool kGru = CELL == PARARNN_LIN_GRU;
+#ifdef FW
+  static constexpr int W = FW, K = FK, S = FS, R = FR;
+#else
   static constexpr int W = 8, K = 8, S = kBF16 ? (kGru ? 3 : 4) : (kGru ? 3 : 2), R = kBF16 && kGru ? 3 : 2;
+#endif
 };
 
 template <int CELL, bool kBF16>
@@ -133,7 +192,9 @@ __global__ void __launch_bounds__(32 * FwdShape<CELL, kBF16>::W, FwdShape<CELL, 
   const bool cok = dbase + cpiece * U::kPiece < p.D;
   const char* src = static_cast<const char*>(p.u) + (b * p.sb + dbase + cpiece * U::kPiece) * ES;
   const uint32_t dst = smem_u32(ring) + warp * Ring::kWarp + crow * G * U::kRow + cpiece * 16;
+  static_assert(K % U::kRows == 0, "whole copies");
   const char* const mine = ring + warp * Ring::kWarp;
+  float4* const cta = reinterpret_cast<float4*>(ring + Ring::kBytes);
   const int round = CL * W * K, first = (rank * W + warp) * K;
   auto copy = [&](int t0, int slot) {  // steps t0 .. t0 + K - 1 of this warp
 #pragma unroll
@@ -156,9 +217,11 @@ __global__ void __launch_bounds__(32 * FwdShape<CELL, kBF16>::W, FwdShape<CELL, 
   cell.init(p.lam, p.bias, p.kappa, p.D, d);
   float2 carry = vec2(p.h0 ? p.h0 + (size_t)b * p.D : nullptr, d);
   const size_t row = (size_t)b * p.T;
-  if (CL > 1) cg::this_cluster().sync();  // every CTA runs before one writes into another
-  int par = 0, slot = 0;
-  for (int base = 0; base < p.T; base += round, par ^= 1) {
+  lin_cluster_start(sh, CL);
+  bool lost = false;
+  int slot = 0;
+  unsigned nround = 0;
+  for (int base = 0; base < p.T; base += round, ++nround) {
     const int t0 = base + first;
     bool mark = false;  // lane j: a reset at step t0 + j
     if (kReset) mark = lane < K && t0 + lane < p.T && p.reset[row + t0 + lane] != 0;
@@ -168,30 +231,38 @@ __global__ void __launch_bounds__(32 * FwdShape<CELL, kBF16>::W, FwdShape<CELL, 
     cp_async_commit();
     const unsigned resets = kReset ? __ballot_sync(0xffffffffu, mark) : 0u;
     const char* rows = mine + slot * Ring::kRound;
+    slot = slot + 1 == S ? 0 : slot + 1;
     // steps past T compute on what the ring holds there: nothing after them is
     // stored
-    float2 nm[K], bb[K], P = both(1.f), Q = both(0.f);
+    float2 P[K], Q[K];  // h after step j is P[j] h_in + Q[j]
 #pragma unroll
     for (int j = 0; j < K; ++j) {
-      float2 u[G];
+      float2 u[G], nm, bb;
 #pragma unroll
       for (int q = 0; q < G; ++q) u[q] = row_pair<kBF16>(rows + (j * G + q) * U::kRow, lane);
-      cell.coef(u, nm[j], bb[j]);
-      Q = lin_step(nm[j], bb[j], Q);
-      P = lfma(nm[j], P, P);
-      if (kReset && ((resets >> j) & 1u)) Q = bb[j];
+      cell.coef(u, nm, bb);
+      P[j] = j ? lfma(nm, P[j - 1], P[j - 1]) : ladd(nm, both(1.f));
+      Q[j] = j ? lin_step(nm, bb, Q[j - 1]) : bb;
+      if (kReset && ((resets >> j) & 1u)) Q[j] = bb;
     }
-    if (kReset && resets) P = both(-1.f);
-    float2 h = lin_exchange<W, kReset>(sh, par, make_float4(P.x, P.y, Q.x, Q.y), warp, rank, CL, lane, carry);
-    float* out = p.h + (row + t0) * p.D + d;
-    const int n = live ? p.T - t0 : 0;
+    float4 map = make_float4(P[K - 1].x, P[K - 1].y, Q[K - 1].x, Q[K - 1].y);
+    if (kReset && resets) map.x = map.y = -1.f;
+    const float2 in = lin_exchange<W, kReset>(sh, cta, nround, map, warp, rank, CL, lane, carry, lost);
 #pragma unroll
     for (int j = 0; j < K; ++j) {
-      h = lin_step(nm[j], bb[j], h);
-      if (kReset && ((resets >> j) & 1u)) h = bb[j];
-      if (j < n) *reinterpret_cast<float2*>(out + (size_t)j * p.D) = h;
+      if (kReset && (resets & ((2u << j) - 1u))) continue;  // nothing is left of h_in
+      Q[j] = lfma(P[j], in, Q[j]);
     }
-    slot = slot + 1 == S ? 0 : slot + 1;
+    float* out = p.h + (row + t0) * p.D + d;
+    if (t0 + K <= p.T) {
+#pragma unroll
+      for (int j = 0; j < K; ++j)
+        if (live) *reinterpret_cast<float2*>(out + (size_t)j * p.D) = Q[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < K; ++j)
+        if (live && t0 + j < p.T) *reinterpret_cast<float2*>(out + (size_t)j * p.D) = Q[j];
+    }
   }
   cp_async_wait<0>();
 }
@@ -201,7 +272,11 @@ __global__ void __launch_bounds__(32 * FwdShape<CELL, kBF16>::W, FwdShape<CELL, 
 template <int CELL, bool kBF16>
 struct BwdShape {
   static constexpr bool kGru = CELL == PARARNN_LIN_GRU;
+#ifdef BW
+  static constexpr int W = BW, K = BK, S = BS, R = BR;
+#else
   static constexpr int W = 8, K = 4, S = kBF16 ? (kGru ? 4 : 3) : (kGru ? 3 : 2), R = 2;
+#endif
 };
 
 template <int CELL, bool kBF16>
@@ -236,11 +311,14 @@ __global__ void __launch_bounds__(32 * BwdShape<CELL, kBF16>::W, BwdShape<CELL, 
   const int crow = lane / U::kLanes, cpiece = lane % U::kLanes;
   const bool cok = dbase + cpiece * U::kPiece < p.D;
   const char* src = static_cast<const char*>(p.u) + (b * p.sb + dbase + cpiece * U::kPiece) * ES;
+  static_assert(K % F::kRows == 0, "whole copies");
   const int frow = lane / F::kLanes, fpiece = lane % F::kLanes;
   const bool fok = dbase + fpiece * F::kPiece < p.D;
   const size_t fcol = row * p.D + dbase + fpiece * F::kPiece;
   const uint32_t dst = smem_u32(ring) + warp * Ring::kWarp;
+  static_assert(K % U::kRows == 0, "whole copies");
   const char* const mine = ring + warp * Ring::kWarp;
+  float4* const cta = reinterpret_cast<float4*>(ring + Ring::kBytes);
   const int round = CL * W * K, first = (rank * W + warp) * K;
   auto copy = [&](int t1, int slot) {  // steps t1 - 1, t1 - 2, ..., t1 - K of this warp
     const uint32_t to = dst + slot * Ring::kRound;
@@ -274,9 +352,11 @@ __global__ void __launch_bounds__(32 * BwdShape<CELL, kBF16>::W, BwdShape<CELL, 
   float2 sum[G + 1];
 #pragma unroll
   for (int q = 0; q <= G; ++q) sum[q] = both(0.f);
-  if (CL > 1) cg::this_cluster().sync();
-  int par = 0, slot = 0;
-  for (int end = p.T; end > 0; end -= round, par ^= 1) {
+  lin_cluster_start(sh, CL);
+  bool lost = false;
+  int slot = 0;
+  unsigned nround = 0;
+  for (int end = p.T; end > 0; end -= round, ++nround) {
     const int t1 = end - first;
     bool mark = false;  // lane j: a reset at step t1 - 1 - j
     if (kReset) mark = lane < K && t1 - 1 - lane >= 0 && p.reset[row + t1 - 1 - lane] != 0;
@@ -299,7 +379,8 @@ __global__ void __launch_bounds__(32 * BwdShape<CELL, kBF16>::W, BwdShape<CELL, 
       if (kReset && ((resets >> j) & 1u)) Q = both(0.f);
     }
     if (kReset && resets) P = both(-1.f);
-    float2 mu = lin_exchange<W, kReset>(sh, par, make_float4(P.x, P.y, Q.x, Q.y), warp, rank, CL, lane, carry);
+    float2 mu = lin_exchange<W, kReset>(sh, cta, nround, make_float4(P.x, P.y, Q.x, Q.y), warp, rank, CL, lane, carry,
+                                        lost);
     float2 add[G + 1];
 #pragma unroll
     for (int q = 0; q <= G; ++q) add[q] = both(0.f);
@@ -408,6 +489,7 @@ __global__ void __launch_bounds__(256) linrec_step(const LinParams p, const floa
 
 template <typename Kern>
 int launch_scan(Kern kern, int threads, int smem, const LinParams& p, int CL, cudaStream_t stream) {
+  if (CL > 1) smem += kLinBufs * CL * 512;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return (int)e;
   cudaLaunchConfig_t cfg = {};

@@ -65,21 +65,24 @@ __device__ __forceinline__ float2 decay_nm(float2 v) {
   return make_float2(v.x < 0.36f ? p.x : e.x, v.y < 0.36f ? p.y : e.y);
 }
 
-// tanh y and the parts of its derivative 1 - tanh^2 = 4 F R^2, F = e^-2|y|,
+// -tanh y and the parts of its derivative 1 - tanh^2 = 4 F R^2, F = e^-2|y|,
 // R = 1 / (1 + F).  Below |y| = 0.3 the Taylor series to y^9 (the next term is
 // below 2^-24 of the sum there), above (1 - F) R with F < 0.55.
-__device__ __forceinline__ float2 tanh_parts(float2 y, float2& F, float2& R) {
+__device__ __forceinline__ float minus_sign_of(float big, float y) {
+  return __uint_as_float(__float_as_uint(big) | (~__float_as_uint(y) & 0x80000000u));
+}
+__device__ __forceinline__ float2 minus_tanh_parts(float2 y, float2& F, float2& R) {
   F = ex2_neg_abs(lmul(y, both(2.f * kLog2e)));
   R = rcp_2(ladd(F, both(1.f)));
   const float2 big = lmul(lfma(F, both(-1.f), both(1.f)), R);
   const float2 s = lmul(y, y);
-  float2 p = lfma(s, both(62.f / 2835.f), both(-17.f / 315.f));
-  p = lfma(s, p, both(2.f / 15.f));
-  p = lfma(s, p, both(-1.f / 3.f));
-  p = lfma(s, p, both(1.f));
+  float2 p = lfma(s, both(-62.f / 2835.f), both(17.f / 315.f));
+  p = lfma(s, p, both(-2.f / 15.f));
+  p = lfma(s, p, both(1.f / 3.f));
+  p = lfma(s, p, both(-1.f));
   p = lmul(y, p);
-  return make_float2(fabsf(y.x) < 0.3f ? p.x : copysignf(big.x, y.x),
-                     fabsf(y.y) < 0.3f ? p.y : copysignf(big.y, y.y));
+  return make_float2(fabsf(y.x) < 0.3f ? p.x : minus_sign_of(big.x, y.x),
+                     fabsf(y.y) < 0.3f ? p.y : minus_sign_of(big.y, y.y));
 }
 
 // log(1 + e^x), once per channel
@@ -111,17 +114,18 @@ struct LinCell<PARARNN_LIN_GRU> {
   __device__ __forceinline__ void coef(const float2 (&u)[G], float2& m, float2& b) const {
     float2 F, R;
     m = nm(u);
-    b = lmul(neg2(m), tanh_parts(ladd(u[1], bc), F, R));
+    b = lmul(m, minus_tanh_parts(ladd(u[1], bc), F, R));
   }
   // du of one step from lambda and h_{t-1}
   __device__ __forceinline__ void grad(const float2 (&u)[G], float2 m, float2 hp, float2 lt, float2 (&du)[G],
                                        float2& /*e*/) const {
     float2 F, R;
-    const float2 c = tanh_parts(ladd(u[1], bc), F, R);
+    const float2 nc = minus_tanh_parts(ladd(u[1], bc), F, R);
     const float2 t = ex2_neg_abs(zarg(u[0])), q = rcp_2(ladd(t, both(1.f)));
-    const float2 zz = lmul(lmul(t, q), q);  // z (1 - z), exact where z is near 1 too
-    du[0] = lmul(lmul(lt, lfma(hp, both(-1.f), c)), zz);
-    du[1] = lmul(lmul(lt, m), lmul(lmul(F, both(-4.f)), lmul(R, R)));
+    const float2 zz = lmul(lmul(t, q), q);  // z (1 - z), where z is near 1 too
+    const float2 nl = neg2(lt);
+    du[0] = lmul(lmul(nl, ladd(hp, nc)), zz);
+    du[1] = lmul(lmul(nl, m), lmul(lmul(F, both(4.f)), lmul(R, R)));
   }
   static __device__ __forceinline__ float2 lam_scale(const float*, int) { return both(0.f); }
 };

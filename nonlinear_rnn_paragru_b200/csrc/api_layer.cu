@@ -9,7 +9,7 @@
 namespace pararnn {
 long long linrec_most_ctas(int B, int D);
 size_t linrec_part_floats(int cell, int B, int T, int D);
-int launch_linrec_fwd(int cell, bool bf16, LinParams p, cudaStream_t stream);
+int launch_linrec_fwd(int cell, bool bf16, const LinParams& p, cudaStream_t stream);
 int launch_linrec_bwd(int cell, bool bf16, bool bf16_out, LinParams p, float* dlam, float* dbias,
                       cudaStream_t stream);
 int launch_linrec_step(int cell, bool bf16, const LinParams& p, const float* h_prev, float* h_next,

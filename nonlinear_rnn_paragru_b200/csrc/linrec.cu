@@ -1,15 +1,17 @@
 // linrec.cu -- the gated linear recurrence: solve (one scan over the
 // sequence), adjoint (one reverse scan) and the single decode step.
 //
-// Layout of the scans.  A cluster of CL CTAs owns a 64-channel tile of one
-// batch row and walks its sequence in rounds of CL x W x K steps (the adjoint
-// from the last step to the first): CTA r, warp w, takes K consecutive steps,
-// lane l the channels 2l and 2l + 1.  In a round a thread composes its steps'
-// maps (P, Q); the W warps' maps meet in shared memory, the CTAs' maps in each
-// other's shared memory (asynchronous stores, two buffers in turn), and every
-// thread composes what precedes its own steps and applies its maps to that.  The state that enters a round stays in a register of
-// every warp.  So each input is read once, each output written once, and
-// nothing waits on global memory: no workspace, no flags, no order of blocks.
+// Layout of the scans.  A cluster of CL CTAs owns a tile of 2 GL channels of
+// one batch row and walks its sequence in rounds (the adjoint from the last
+// step to the first).  A thread owns two neighbouring channels; GL lanes are a
+// group, and the groups of a round take K consecutive steps each, in the order
+// of the scan: CTA, warp, group of the warp.  In a round a thread composes its
+// steps' maps (P, Q); the groups' maps meet in shared memory, the CTAs' maps in
+// each other's shared memory (asynchronous stores), in two buffers in turn, and
+// every thread composes what precedes its own steps and applies its maps to
+// that.  The state that enters a round stays in a register of every thread.  So
+// each input is read once, each output written once, and nothing waits on
+// global memory: no workspace, no flags, no order of blocks.
 //
 // Every warp copies its own rows into a ring of S rounds in shared memory
 // (16-byte cp.async, S - 1 rounds ahead), which keeps HBM busy through the
@@ -25,7 +27,6 @@ namespace cg = cooperative_groups;
 namespace pararnn {
 namespace {
 
-constexpr int kLinTile = 64;  // channels of a tile
 constexpr int kLinMaxCluster = 8;
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
@@ -37,23 +38,31 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// One kind of row in a warp's ring: 64 channels of kBytes each, 16 bytes a
-// lane, so an instruction moves kRows rows.
-template <int kBytes>
+// One kind of row in a warp's ring: C rows (gates) a step, of a tile's 2 GL
+// channels of kBytes each.  A round of a warp holds, per group, K steps and a
+// row of padding (the groups' rows then lie in different banks).  An
+// instruction moves kRows steps' rows, 16 bytes a lane.
+template <int GL, int K, int C, int kBytes>
 struct Rows {
-  static constexpr int kRow = 64 * kBytes;       // bytes of a row
+  static constexpr int kNG = 32 / GL;
+  static constexpr int kRow = 2 * GL * kBytes;   // bytes of a row
   static constexpr int kLanes = kRow / 16;       // lanes of a row
   static constexpr int kRows = 32 / kLanes;
   static constexpr int kPiece = 16 / kBytes;     // channels of a lane
+  static constexpr int kGroup = K * C * kRow + (kNG > 1 ? kRow : 0);
+  static constexpr int kRound = kNG * kGroup;
+  static constexpr int kCopies = kNG * K / kRows;
+  static_assert(kCopies * kRows == kNG * K && (K % kRows == 0 || kRows % K == 0), "whole copies");
+  // where step i (of a warp's kNG K, in the order of the scan) lies
+  static __host__ __device__ constexpr int at(int i) { return i / K * kGroup + i % K * C * kRow; }
 };
 
-// The warps' maps of a round, and the mbarriers that count the arrival of the
-// CTAs' maps; those lie in dynamic shared memory, kLinBufs x CL x 512 bytes.
-constexpr int kLinBufs = 2;
+// The groups' maps of a round, and the mbarriers that count the arrival of the
+// CTAs' maps; those lie in dynamic shared memory, 2 x CL x GL x 16 bytes.
 template <int W>
 struct LinShared {
-  float4 warp[2][W][32];
-  uint64_t bar[kLinBufs];
+  float4 map[2][W * 32];
+  uint64_t bar[2];
 };
 
 __device__ __forceinline__ uint32_t map_rank(uint32_t addr, int rank) {
@@ -73,11 +82,11 @@ __device__ __forceinline__ void st_async16(uint32_t addr, uint32_t bar, float4 v
 
 constexpr uint64_t kLinWaitNs = 2000000000ull;
 
-template <int CL, bool kReset>
-__device__ __forceinline__ float2 lin_join(const float4* cta, int rpos, int lane, float2& carry) {
+template <int CL, int GL, bool kReset>
+__device__ __forceinline__ float2 lin_join(const float4* cta, int rpos, int gl, float2& carry) {
   float4 v[CL];
 #pragma unroll
-  for (int i = 0; i < CL; ++i) v[i] = cta[i * 32 + lane];
+  for (int i = 0; i < CL; ++i) v[i] = cta[i * GL + gl];
   float2 in = carry;
 #pragma unroll
   for (int i = 0; i < CL; ++i) {
@@ -87,51 +96,53 @@ __device__ __forceinline__ float2 lin_join(const float4* cta, int rpos, int lane
   return in;
 }
 
-// Publish the warp's map of round r and return the state that enters this
-// thread's steps; `carry`, the state that enters the round, becomes the one
-// that leaves it.  Positions (wpos of the warp, rpos of the CTA) run in the
+// Publish the thread's map of round r and return the state that enters its
+// steps; `carry`, the state that enters the round, becomes the one that leaves
+// it.  Positions (gpos of the group in the CTA, rpos of the CTA) run in the
 // order of the scan.  Buffers and mbarriers alternate: a CTA can only send the
 // maps of round r + 2 after every CTA's of round r + 1 came, which each sends
 // after all its warps have read those of round r.  The wait for the cluster is
 // bounded; where it runs out the states become NaN.
-template <int W, bool kReset>
-__device__ __forceinline__ float2 lin_exchange(LinShared<W>& sh, float4* cta, unsigned r, float4 mine, int wpos,
-                                               int rpos, int CL, int lane, float2& carry, bool& lost) {
-  const int par = r & 1;
-  sh.warp[par][wpos][lane] = mine;
+template <int W, int GL, bool kReset>
+__device__ __forceinline__ float2 lin_exchange(LinShared<W>& sh, float4* cta, unsigned r, float4 mine, int rpos,
+                                               int CL, float2& carry, bool& lost) {
+  constexpr int NP = W * 32 / GL;
+  const int par = r & 1, gl = threadIdx.x % GL, gpos = threadIdx.x / GL;
+  sh.map[par][threadIdx.x] = mine;
   __syncthreads();
-  float4 v[W];
-#pragma unroll
-  for (int i = 0; i < W; ++i) v[i] = sh.warp[par][i][lane];
+  const float4* maps = sh.map[par] + gl;
   float2 in = carry;
   if (CL == 1) {
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-      if (i == wpos) in = carry;
-      carry = lin_apply<kReset>(v[i], carry);
+    for (int i = 0; i < NP; ++i) {
+      if (i == gpos) in = carry;
+      carry = lin_apply<kReset>(maps[i * GL], carry);
     }
     return in;
   }
   float4 before = make_float4(1.f, 1.f, 0.f, 0.f);
 #pragma unroll
-  for (int i = 0; i < W - 1; ++i)
-    if (i < wpos) before = i ? lin_then<kReset>(before, v[i]) : v[0];
-  if (wpos == W - 1) {
+  for (int i = 0; i < NP - 1; ++i) {
+    const float4 v = maps[i * GL];
+    if (i < gpos) before = i ? lin_then<kReset>(before, v) : v;
+  }
+  if (gpos == NP - 1) {
     const float4 all = lin_then<kReset>(before, mine);
-    if (lane == 0) mbar_arrive_expect_tx(&sh.bar[par], CL * 512);
-    const uint32_t at = smem_u32(&cta[(par * CL + rpos) * 32 + lane]), bar = smem_u32(&sh.bar[par]);
+    if (gl == 0) mbar_arrive_expect_tx(&sh.bar[par], CL * GL * 16);
+    const uint32_t at = smem_u32(&cta[(par * CL + rpos) * GL + gl]), bar = smem_u32(&sh.bar[par]);
     for (int i = 0; i < CL; ++i) st_async16(map_rank(at, i), map_rank(bar, i), all);
   }
+  __syncwarp();
   if (!lost) lost = !mbar_wait_bounded(&sh.bar[par], (r >> 1) & 1, kLinWaitNs);
-  const float4* maps = cta + par * CL * 32;
+  const float4* v = cta + par * CL * GL;
   if (CL == 2)
-    in = lin_join<2, kReset>(maps, rpos, lane, carry);
+    in = lin_join<2, GL, kReset>(v, rpos, gl, carry);
   else if (CL == 4)
-    in = lin_join<4, kReset>(maps, rpos, lane, carry);
+    in = lin_join<4, GL, kReset>(v, rpos, gl, carry);
   else
-    in = lin_join<8, kReset>(maps, rpos, lane, carry);
+    in = lin_join<8, GL, kReset>(v, rpos, gl, carry);
   if (lost) carry = in = both(__int_as_float(0x7fffffff));
-  return wpos ? lin_apply<kReset>(before, in) : in;
+  return gpos ? lin_apply<kReset>(before, in) : in;
 }
 
 // Before the rounds: the mbarriers, and every CTA of the cluster runs before
@@ -140,8 +151,23 @@ template <int W>
 __device__ __forceinline__ void lin_cluster_start(LinShared<W>& sh, int CL) {
   if (CL == 1) return;
   if (threadIdx.x == 0)
-    for (int i = 0; i < kLinBufs; ++i) mbar_init(&sh.bar[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&sh.bar[i], 1);
   cg::this_cluster().sync();
+}
+
+// A group's marked steps: bit j for its j-th step of the scan, `step` of which
+// is at reset[at + dir * j], `n` of them within the sequence.
+template <int GL, int K>
+__device__ __forceinline__ unsigned lin_marks(const unsigned char* at, int dir, int n) {
+  const int gl = threadIdx.x % GL, shift = threadIdx.x % 32 / GL * GL;
+  unsigned bits = 0;
+#pragma unroll
+  for (int m = 0; m < K; m += GL) {
+    const bool mark = gl + m < min(K, n) && at[(long long)dir * (gl + m)] != 0;
+    const unsigned all = __ballot_sync(0xffffffffu, mark) >> shift;
+    bits |= (GL == 32 ? all : all & ((1u << (GL % 32)) - 1u)) << m;
+  }
+  return bits;
 }
 
 // Shape of a scan kernel: W warps, K steps of a thread in a round, a ring of S
@@ -150,19 +176,14 @@ template <int CELL, bool kBF16>
 struct FwdShape {
   static constexpr bool kGru = CELL == PARARNN_LIN_GRU;
 #ifdef FW
-  static constexpr int W = FW, K = FK, S = FS, R = FR;
+  static constexpr int GL = FG, W = FW, K = FK, S = FS, R = FR;
 #else
-  static constexpr int W = 8, K = 8, S = kBF16 ? (kGru ? 3 : 4) : (kGru ? 3 : 2), R = kBF16 && kGru ? 3 : 2;
+  static constexpr int GL = 32, W = 4, K = kBF16 && kGru ? 8 : 16, S = kBF16 && kGru ? 3 : 2,
+                       R = kBF16 && kGru ? 5 : kBF16 || kGru ? 3 : 2;
 #endif
-};
-
-template <int CELL, bool kBF16>
-struct FwdRing {
-  using U = Rows<kBF16 ? 2 : 4>;
-  static constexpr int K = FwdShape<CELL, kBF16>::K, G = LinCell<CELL>::G;
-  static constexpr int kRound = K * G * U::kRow;  // bytes of a warp's round
-  static constexpr int kWarp = FwdShape<CELL, kBF16>::S * kRound;
-  static constexpr int kBytes = FwdShape<CELL, kBF16>::W * kWarp;
+  using U = Rows<GL, K, LinCell<CELL>::G, kBF16 ? 2 : 4>;
+  static constexpr int kWarp = S * U::kRound;   // bytes of a warp's ring
+  static constexpr int kBytes = W * kWarp;
 };
 
 template <bool kBF16>
@@ -176,33 +197,33 @@ __global__ void __launch_bounds__(32 * FwdShape<CELL, kBF16>::W, FwdShape<CELL, 
     linrec_fwd(const LinParams p, const int CL) {
   using Cell = LinCell<CELL>;
   using Shape = FwdShape<CELL, kBF16>;
-  using Ring = FwdRing<CELL, kBF16>;
-  using U = typename Ring::U;
-  constexpr int G = Cell::G, K = Shape::K, W = Shape::W, S = Shape::S, ES = kBF16 ? 2 : 4;
+  using U = typename Shape::U;
+  constexpr int G = Cell::G, K = Shape::K, W = Shape::W, S = Shape::S, GL = Shape::GL, ES = kBF16 ? 2 : 4;
+  constexpr int KW = U::kNG * K;  // steps of a warp in a round
   extern __shared__ __align__(16) char ring[];
   __shared__ LinShared<W> sh;
   const int rank = CL > 1 ? (int)cg::this_cluster().block_rank() : 0;
   const int tile = blockIdx.x / CL;
   const int b = tile / p.ntd, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int dbase = (tile - b * p.ntd) * kLinTile, d0 = dbase + 2 * lane;
+  const int gl = lane % GL, grp = lane / GL;
+  const int dbase = (tile - b * p.ntd) * 2 * GL, d0 = dbase + 2 * gl;
   const bool live = d0 < p.D;
   const int d = live ? d0 : p.D - 2;  // idle lanes read parameters that exist
   // copies: this lane's row of an instruction and its piece of the row
   const int crow = lane / U::kLanes, cpiece = lane % U::kLanes;
   const bool cok = dbase + cpiece * U::kPiece < p.D;
   const char* src = static_cast<const char*>(p.u) + (b * p.sb + dbase + cpiece * U::kPiece) * ES;
-  const uint32_t dst = smem_u32(ring) + warp * Ring::kWarp + crow * G * U::kRow + cpiece * 16;
-  static_assert(K % U::kRows == 0, "whole copies");
-  const char* const mine = ring + warp * Ring::kWarp;
-  float4* const cta = reinterpret_cast<float4*>(ring + Ring::kBytes);
-  const int round = CL * W * K, first = (rank * W + warp) * K;
-  auto copy = [&](int t0, int slot) {  // steps t0 .. t0 + K - 1 of this warp
+  const uint32_t dst = smem_u32(ring) + warp * Shape::kWarp + U::at(crow) + cpiece * 16;
+  const char* const mine = ring + warp * Shape::kWarp + U::at(grp * K);
+  float4* const cta = reinterpret_cast<float4*>(ring + Shape::kBytes);
+  const int round = CL * W * KW, first = (rank * W + warp) * KW;
+  auto copy = [&](int tw, int slot) {  // steps tw .. tw + KW - 1
 #pragma unroll
-    for (int i = 0; i < K; i += U::kRows) {
-      const int t = t0 + i + crow;
+    for (int i = 0; i < U::kCopies; ++i) {
+      const int t = tw + i * U::kRows + crow;
       if (cok && t < p.T) {
         const char* s = src + t * (p.st * ES);
-        const uint32_t o = dst + slot * Ring::kRound + i * G * U::kRow;
+        const uint32_t o = dst + slot * U::kRound + U::at(i * U::kRows);
 #pragma unroll
         for (int q = 0; q < G; ++q) cp_async16(o + q * U::kRow, s + q * (p.sg * ES));
       }
@@ -222,15 +243,13 @@ __global__ void __launch_bounds__(32 * FwdShape<CELL, kBF16>::W, FwdShape<CELL, 
   int slot = 0;
   unsigned nround = 0;
   for (int base = 0; base < p.T; base += round, ++nround) {
-    const int t0 = base + first;
-    bool mark = false;  // lane j: a reset at step t0 + j
-    if (kReset) mark = lane < K && t0 + lane < p.T && p.reset[row + t0 + lane] != 0;
+    const int tw = base + first, t0 = tw + grp * K;
     cp_async_wait<S - 2>();
     __syncwarp();
-    copy(t0 + (S - 1) * round, slot == 0 ? S - 1 : slot - 1);
+    copy(tw + (S - 1) * round, slot == 0 ? S - 1 : slot - 1);
     cp_async_commit();
-    const unsigned resets = kReset ? __ballot_sync(0xffffffffu, mark) : 0u;
-    const char* rows = mine + slot * Ring::kRound;
+    const unsigned resets = kReset ? lin_marks<GL, K>(p.reset + row + t0, 1, p.T - t0) : 0u;
+    const char* rows = mine + slot * U::kRound;
     slot = slot + 1 == S ? 0 : slot + 1;
     // steps past T compute on what the ring holds there: nothing after them is
     // stored
@@ -239,7 +258,7 @@ __global__ void __launch_bounds__(32 * FwdShape<CELL, kBF16>::W, FwdShape<CELL, 
     for (int j = 0; j < K; ++j) {
       float2 u[G], nm, bb;
 #pragma unroll
-      for (int q = 0; q < G; ++q) u[q] = row_pair<kBF16>(rows + (j * G + q) * U::kRow, lane);
+      for (int q = 0; q < G; ++q) u[q] = row_pair<kBF16>(rows + (j * G + q) * U::kRow, gl);
       cell.coef(u, nm, bb);
       P[j] = j ? lfma(nm, P[j - 1], P[j - 1]) : ladd(nm, both(1.f));
       Q[j] = j ? lin_step(nm, bb, Q[j - 1]) : bb;
@@ -247,11 +266,11 @@ __global__ void __launch_bounds__(32 * FwdShape<CELL, kBF16>::W, FwdShape<CELL, 
     }
     float4 map = make_float4(P[K - 1].x, P[K - 1].y, Q[K - 1].x, Q[K - 1].y);
     if (kReset && resets) map.x = map.y = -1.f;
-    const float2 in = lin_exchange<W, kReset>(sh, cta, nround, map, warp, rank, CL, lane, carry, lost);
+    const float2 in = lin_exchange<W, GL, kReset>(sh, cta, nround, map, rank, CL, carry, lost);
 #pragma unroll
     for (int j = 0; j < K; ++j) {
-      if (kReset && (resets & ((2u << j) - 1u))) continue;  // nothing is left of h_in
-      Q[j] = lfma(P[j], in, Q[j]);
+      const float2 h = lfma(P[j], in, Q[j]);
+      if (!kReset || !(resets & ((2u << j) - 1u))) Q[j] = h;  // after a reset nothing is left of h_in
     }
     float* out = p.h + (row + t0) * p.D + d;
     if (t0 + K <= p.T) {
@@ -273,21 +292,16 @@ template <int CELL, bool kBF16>
 struct BwdShape {
   static constexpr bool kGru = CELL == PARARNN_LIN_GRU;
 #ifdef BW
-  static constexpr int W = BW, K = BK, S = BS, R = BR;
+  static constexpr int GL = BG, W = BW, K = BK, S = BS, R = BR;
 #else
-  static constexpr int W = 8, K = 4, S = kBF16 ? (kGru ? 4 : 3) : (kGru ? 3 : 2), R = 2;
+  static constexpr int GL = 32, W = 4, K = 4, S = kBF16 ? 3 : 2, R = 4;
 #endif
-};
-
-template <int CELL, bool kBF16>
-struct BwdRing {
-  using U = Rows<kBF16 ? 2 : 4>;
-  using F = Rows<4>;
-  static constexpr int K = BwdShape<CELL, kBF16>::K, G = LinCell<CELL>::G;
-  static constexpr int kH = K * G * U::kRow, kG = kH + K * F::kRow;  // offsets of h_{t-1}, dL/dh
-  static constexpr int kRound = kG + K * F::kRow;
-  static constexpr int kWarp = BwdShape<CELL, kBF16>::S * kRound;
-  static constexpr int kBytes = BwdShape<CELL, kBF16>::W * kWarp;
+  using U = Rows<GL, K, LinCell<CELL>::G, kBF16 ? 2 : 4>;
+  using F = Rows<GL, K, 1, 4>;
+  static constexpr int kH = U::kRound, kG = kH + F::kRound;  // offsets of h_{t-1} and dL/dh in a round
+  static constexpr int kRound = kG + F::kRound;
+  static constexpr int kWarp = S * kRound;
+  static constexpr int kBytes = W * kWarp;
 };
 
 template <int CELL, bool kBF16, bool kBF16Out, bool kReset>
@@ -295,49 +309,49 @@ __global__ void __launch_bounds__(32 * BwdShape<CELL, kBF16>::W, BwdShape<CELL, 
     linrec_bwd(const LinParams p, const int CL) {
   using Cell = LinCell<CELL>;
   using Shape = BwdShape<CELL, kBF16>;
-  using Ring = BwdRing<CELL, kBF16>;
-  using U = typename Ring::U;
-  using F = typename Ring::F;
-  constexpr int G = Cell::G, K = Shape::K, W = Shape::W, S = Shape::S, ES = kBF16 ? 2 : 4;
+  using U = typename Shape::U;
+  using F = typename Shape::F;
+  constexpr int G = Cell::G, K = Shape::K, W = Shape::W, S = Shape::S, GL = Shape::GL, ES = kBF16 ? 2 : 4;
+  constexpr int KW = U::kNG * K;
   extern __shared__ __align__(16) char ring[];
   __shared__ LinShared<W> sh;
   const int rank = CL > 1 ? (int)cg::this_cluster().block_rank() : 0;
   const int tile = blockIdx.x / CL;
   const int b = tile / p.ntd, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int dbase = (tile - b * p.ntd) * kLinTile, d0 = dbase + 2 * lane;
+  const int gl = lane % GL, grp = lane / GL;
+  const int dbase = (tile - b * p.ntd) * 2 * GL, d0 = dbase + 2 * gl;
   const bool live = d0 < p.D;
   const int d = live ? d0 : p.D - 2;
   const size_t row = (size_t)b * p.T;
   const int crow = lane / U::kLanes, cpiece = lane % U::kLanes;
   const bool cok = dbase + cpiece * U::kPiece < p.D;
   const char* src = static_cast<const char*>(p.u) + (b * p.sb + dbase + cpiece * U::kPiece) * ES;
-  static_assert(K % F::kRows == 0, "whole copies");
   const int frow = lane / F::kLanes, fpiece = lane % F::kLanes;
   const bool fok = dbase + fpiece * F::kPiece < p.D;
   const size_t fcol = row * p.D + dbase + fpiece * F::kPiece;
-  const uint32_t dst = smem_u32(ring) + warp * Ring::kWarp;
-  static_assert(K % U::kRows == 0, "whole copies");
-  const char* const mine = ring + warp * Ring::kWarp;
-  float4* const cta = reinterpret_cast<float4*>(ring + Ring::kBytes);
-  const int round = CL * W * K, first = (rank * W + warp) * K;
-  auto copy = [&](int t1, int slot) {  // steps t1 - 1, t1 - 2, ..., t1 - K of this warp
-    const uint32_t to = dst + slot * Ring::kRound;
+  const uint32_t udst = smem_u32(ring) + warp * Shape::kWarp + U::at(crow) + cpiece * 16;
+  const uint32_t fdst = smem_u32(ring) + warp * Shape::kWarp + F::at(frow) + fpiece * 16;
+  const char* const umine = ring + warp * Shape::kWarp + U::at(grp * K);
+  const char* const fmine = ring + warp * Shape::kWarp + F::at(grp * K);
+  float4* const cta = reinterpret_cast<float4*>(ring + Shape::kBytes);
+  const int round = CL * W * KW, first = (rank * W + warp) * KW;
+  auto copy = [&](int tw, int slot) {  // steps tw - 1, tw - 2, ..., tw - KW
 #pragma unroll
-    for (int i = 0; i < K; i += U::kRows) {
-      const int t = t1 - 1 - i - crow;
+    for (int i = 0; i < U::kCopies; ++i) {
+      const int t = tw - 1 - i * U::kRows - crow;
       if (cok && t >= 0) {
         const char* s = src + t * (p.st * ES);
-        const uint32_t o = to + (i + crow) * G * U::kRow + cpiece * 16;
+        const uint32_t o = udst + slot * Shape::kRound + U::at(i * U::kRows);
 #pragma unroll
         for (int q = 0; q < G; ++q) cp_async16(o + q * U::kRow, s + q * (p.sg * ES));
       }
     }
 #pragma unroll
-    for (int i = 0; i < K; i += F::kRows) {
-      const int t = t1 - 1 - i - frow;
-      const uint32_t o = to + (i + frow) * F::kRow + fpiece * 16;
-      if (fok && t >= 0) cp_async16(o + Ring::kG, p.g + fcol + (size_t)t * p.D);
-      if (fok && t >= 1) cp_async16(o + Ring::kH, p.h + fcol + (size_t)(t - 1) * p.D);
+    for (int i = 0; i < F::kCopies; ++i) {
+      const int t = tw - 1 - i * F::kRows - frow;
+      const uint32_t o = fdst + slot * Shape::kRound + F::at(i * F::kRows);
+      if (fok && t >= 0) cp_async16(o + Shape::kG, p.g + fcol + (size_t)t * p.D);
+      if (fok && t >= 1) cp_async16(o + Shape::kH, p.h + fcol + (size_t)(t - 1) * p.D);
     }
   };
 #pragma unroll
@@ -357,45 +371,45 @@ __global__ void __launch_bounds__(32 * BwdShape<CELL, kBF16>::W, BwdShape<CELL, 
   int slot = 0;
   unsigned nround = 0;
   for (int end = p.T; end > 0; end -= round, ++nround) {
-    const int t1 = end - first;
-    bool mark = false;  // lane j: a reset at step t1 - 1 - j
-    if (kReset) mark = lane < K && t1 - 1 - lane >= 0 && p.reset[row + t1 - 1 - lane] != 0;
+    const int tw = end - first, t1 = tw - grp * K;  // this thread's steps: t1 - 1, ..., t1 - K
     cp_async_wait<S - 2>();
     __syncwarp();
-    copy(t1 - (S - 1) * round, slot == 0 ? S - 1 : slot - 1);
+    copy(tw - (S - 1) * round, slot == 0 ? S - 1 : slot - 1);
     cp_async_commit();
-    const unsigned resets = kReset ? __ballot_sync(0xffffffffu, mark) : 0u;
-    const char* rows = mine + slot * Ring::kRound;
+    const unsigned resets = kReset ? lin_marks<GL, K>(p.reset + row + t1 - 1, -1, t1) : 0u;
+    const char* urows = umine + slot * Shape::kRound;
+    const char* grows = fmine + slot * Shape::kRound + Shape::kG;
+    const char* hrows = fmine + slot * Shape::kRound + Shape::kH;
+    slot = slot + 1 == S ? 0 : slot + 1;
     float2 nm[K], P = both(1.f), Q = both(0.f);
 #pragma unroll
     for (int j = 0; j < K; ++j) {
       float2 u[G];
 #pragma unroll
-      for (int q = 0; q < G; ++q) u[q] = row_pair<kBF16>(rows + (j * G + q) * U::kRow, lane);
+      for (int q = 0; q < G; ++q) u[q] = row_pair<kBF16>(urows + (j * G + q) * U::kRow, gl);
       nm[j] = cell.nm(u);
-      const float2 lt = ladd(row_pair<false>(rows + Ring::kG + j * F::kRow, lane), Q);
+      const float2 lt = ladd(row_pair<false>(grows + j * F::kRow, gl), Q);
       Q = lfma(nm[j], lt, lt);
       P = lfma(nm[j], P, P);
       if (kReset && ((resets >> j) & 1u)) Q = both(0.f);
     }
     if (kReset && resets) P = both(-1.f);
-    float2 mu = lin_exchange<W, kReset>(sh, cta, nround, make_float4(P.x, P.y, Q.x, Q.y), warp, rank, CL, lane, carry,
-                                        lost);
+    float2 mu = lin_exchange<W, GL, kReset>(sh, cta, nround, make_float4(P.x, P.y, Q.x, Q.y), rank, CL, carry, lost);
     float2 add[G + 1];
 #pragma unroll
     for (int q = 0; q <= G; ++q) add[q] = both(0.f);
 #pragma unroll
     for (int j = 0; j < K; ++j) {
       const int t = t1 - 1 - j;
-      if (t < 0) break;  // a warp's steps before the sequence: all that follow too
+      if (t < 0) break;  // steps before the sequence: all that follow too
       const bool rs = kReset && ((resets >> j) & 1u);
-      const float2 lt = ladd(row_pair<false>(rows + Ring::kG + j * F::kRow, lane), mu);
+      const float2 lt = ladd(row_pair<false>(grows + j * F::kRow, gl), mu);
       mu = rs ? both(0.f) : lfma(nm[j], lt, lt);
-      float2 hp = t == 0 ? h0 : row_pair<false>(rows + Ring::kH + j * F::kRow, lane);
+      float2 hp = t == 0 ? h0 : row_pair<false>(hrows + j * F::kRow, gl);
       if (rs) hp = both(0.f);
       float2 u[G], du[G], e;
 #pragma unroll
-      for (int q = 0; q < G; ++q) u[q] = row_pair<kBF16>(rows + (j * G + q) * U::kRow, lane);
+      for (int q = 0; q < G; ++q) u[q] = row_pair<kBF16>(urows + (j * G + q) * U::kRow, gl);
       cell.grad(u, nm[j], hp, lt, du, e);
       const size_t at = ((row + t) * G) * p.D + d;
 #pragma unroll
@@ -418,22 +432,21 @@ __global__ void __launch_bounds__(32 * BwdShape<CELL, kBF16>::W, BwdShape<CELL, 
     // error grows with the number of rounds only
 #pragma unroll
     for (int q = 0; q <= G; ++q) sum[q] = ladd(sum[q], add[q]);
-    slot = slot + 1 == S ? 0 : slot + 1;
   }
   cp_async_wait<0>();
   if (!p.part) return;
   if (CELL == PARARNN_LIN_DECAY) sum[G] = lmul(sum[G], Cell::lam_scale(p.lam, d));
-  // the warps' sums, in warp order
+  // the groups' sums, in their order
   __syncthreads();
-  float2* const acc = reinterpret_cast<float2*>(ring);  // [warp][G + 1][32]
-  static_assert(Ring::kBytes >= W * (G + 1) * 32 * (int)sizeof(float2), "sums fit");
+  float2* const acc = reinterpret_cast<float2*>(ring);  // [G + 1][W * 32]
+  static_assert(Shape::kBytes >= W * (G + 1) * 32 * (int)sizeof(float2), "sums fit");
   static_assert(W > G, "a warp for each sum");
 #pragma unroll
-  for (int q = 0; q <= G; ++q) acc[(warp * (G + 1) + q) * 32 + lane] = sum[q];
+  for (int q = 0; q <= G; ++q) acc[q * W * 32 + threadIdx.x] = sum[q];
   __syncthreads();
-  if (warp <= G && live) {
+  if (warp <= G && lane < GL && live) {
     float2 s = both(0.f);
-    for (int i = 0; i < W; ++i) s = ladd(s, acc[(i * (G + 1) + warp) * 32 + lane]);
+    for (int i = 0; i < W * 32 / GL; ++i) s = ladd(s, acc[warp * W * 32 + i * GL + lane]);
     float* q = p.part + ((size_t)(b * CL + rank) * (G + 1) + warp) * p.D + d;
     q[0] = s.x;
     q[1] = s.y;
@@ -488,8 +501,9 @@ __global__ void __launch_bounds__(256) linrec_step(const LinParams p, const floa
 }
 
 template <typename Kern>
-int launch_scan(Kern kern, int threads, int smem, const LinParams& p, int CL, cudaStream_t stream) {
-  if (CL > 1) smem += kLinBufs * CL * 512;
+int launch_scan(Kern kern, int GL, int threads, int smem, LinParams p, int CL, cudaStream_t stream) {
+  p.ntd = (p.D + 2 * GL - 1) / (2 * GL);
+  if (CL > 1) smem += 2 * CL * GL * 16;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return (int)e;
   cudaLaunchConfig_t cfg = {};
@@ -507,47 +521,43 @@ int launch_scan(Kern kern, int threads, int smem, const LinParams& p, int CL, cu
   return (int)cudaLaunchKernelEx(&cfg, kern, p, CL);
 }
 
-template <int CELL, bool kBF16>
-int launch_fwd_t(const LinParams& p, int CL, cudaStream_t stream) {
-  constexpr int threads = 32 * FwdShape<CELL, kBF16>::W, smem = FwdRing<CELL, kBF16>::kBytes;
-  return p.reset ? launch_scan(linrec_fwd<CELL, kBF16, true>, threads, smem, p, CL, stream)
-                 : launch_scan(linrec_fwd<CELL, kBF16, false>, threads, smem, p, CL, stream);
-}
-
-template <int CELL, bool kBF16, bool kBF16Out>
-int launch_bwd_t(const LinParams& p, int CL, cudaStream_t stream) {
-  constexpr int threads = 32 * BwdShape<CELL, kBF16>::W, smem = BwdRing<CELL, kBF16>::kBytes;
-  return p.reset ? launch_scan(linrec_bwd<CELL, kBF16, kBF16Out, true>, threads, smem, p, CL, stream)
-                 : launch_scan(linrec_bwd<CELL, kBF16, kBF16Out, false>, threads, smem, p, CL, stream);
-}
-
-template <int CELL>
-int launch_bwd_c(bool bf16, bool bf16_out, const LinParams& p, int CL, cudaStream_t stream) {
-  if (!bf16) return launch_bwd_t<CELL, false, false>(p, CL, stream);
-  return bf16_out ? launch_bwd_t<CELL, true, true>(p, CL, stream) : launch_bwd_t<CELL, true, false>(p, CL, stream);
-}
-
 // CTAs of a cluster: as many as fill one wave of `per_sm` CTAs on 148 SMs, no
 // more than the sequence has rounds of one CTA (`steps`) for.
-int cluster_for(int B, int T, int D, int per_sm, int steps) {
-  const long long tiles = (long long)B * ((D + kLinTile - 1) / kLinTile);
+int cluster_for(int B, int T, int D, int GL, int per_sm, int steps) {
+  const long long tiles = (long long)B * ((D + 2 * GL - 1) / (2 * GL));
   int CL = 1;
   while (CL < kLinMaxCluster && 2 * tiles * CL <= 148 * per_sm && T > CL * steps) CL *= 2;
   return CL;
 }
 
-template <int CELL>
-int fwd_cluster(bool bf16, int B, int T, int D) {
-  using H = FwdShape<CELL, true>;
-  using F = FwdShape<CELL, false>;
-  return bf16 ? cluster_for(B, T, D, H::R, H::W * H::K) : cluster_for(B, T, D, F::R, F::W * F::K);
+template <int CELL, bool kBF16>
+int launch_fwd_t(const LinParams& p, cudaStream_t stream) {
+  using H = FwdShape<CELL, kBF16>;
+  const int CL = cluster_for(p.B, p.T, p.D, H::GL, H::R, H::W * H::U::kNG * H::K);
+  return p.reset ? launch_scan(linrec_fwd<CELL, kBF16, true>, H::GL, 32 * H::W, H::kBytes, p, CL, stream)
+                 : launch_scan(linrec_fwd<CELL, kBF16, false>, H::GL, 32 * H::W, H::kBytes, p, CL, stream);
 }
 
 // the same for both types of u, so that the workspace does not depend on it
 template <int CELL>
 int bwd_cluster(int B, int T, int D) {
   using H = BwdShape<CELL, true>;
-  return cluster_for(B, T, D, H::R, H::W * H::K);
+  static_assert(H::GL == BwdShape<CELL, false>::GL, "one tile width");
+  return cluster_for(B, T, D, H::GL, H::R, H::W * H::U::kNG * H::K);
+}
+
+template <int CELL, bool kBF16, bool kBF16Out>
+int launch_bwd_t(const LinParams& p, cudaStream_t stream) {
+  using H = BwdShape<CELL, kBF16>;
+  const int CL = bwd_cluster<CELL>(p.B, p.T, p.D);
+  return p.reset ? launch_scan(linrec_bwd<CELL, kBF16, kBF16Out, true>, H::GL, 32 * H::W, H::kBytes, p, CL, stream)
+                 : launch_scan(linrec_bwd<CELL, kBF16, kBF16Out, false>, H::GL, 32 * H::W, H::kBytes, p, CL, stream);
+}
+
+template <int CELL>
+int launch_bwd_c(bool bf16, bool bf16_out, const LinParams& p, cudaStream_t stream) {
+  if (!bf16) return launch_bwd_t<CELL, false, false>(p, stream);
+  return bf16_out ? launch_bwd_t<CELL, true, true>(p, stream) : launch_bwd_t<CELL, true, false>(p, stream);
 }
 
 }  // namespace
@@ -556,37 +566,29 @@ int linrec_bwd_cluster(int cell, int B, int T, int D) {
   return cell == PARARNN_LIN_GRU ? bwd_cluster<PARARNN_LIN_GRU>(B, T, D) : bwd_cluster<PARARNN_LIN_DECAY>(B, T, D);
 }
 
-long long linrec_most_ctas(int B, int D) {
-  return (long long)B * ((D + kLinTile - 1) / kLinTile) * kLinMaxCluster;
-}
+// more CTAs than any launch for this problem has (tiles of at least 8 channels)
+long long linrec_most_ctas(int B, int D) { return (long long)B * (D / 8) * kLinMaxCluster; }
 
 size_t linrec_part_floats(int cell, int B, int T, int D) {
   return (size_t)B * linrec_bwd_cluster(cell, B, T, D) * (cell == PARARNN_LIN_GRU ? 3 : 4) * D;
 }
 
-int launch_linrec_fwd(int cell, bool bf16, LinParams p, cudaStream_t stream) {
-  p.ntd = (p.D + kLinTile - 1) / kLinTile;
-  if (cell == PARARNN_LIN_GRU) {
-    const int CL = fwd_cluster<PARARNN_LIN_GRU>(bf16, p.B, p.T, p.D);
-    return bf16 ? launch_fwd_t<PARARNN_LIN_GRU, true>(p, CL, stream)
-                : launch_fwd_t<PARARNN_LIN_GRU, false>(p, CL, stream);
-  }
-  const int CL = fwd_cluster<PARARNN_LIN_DECAY>(bf16, p.B, p.T, p.D);
-  return bf16 ? launch_fwd_t<PARARNN_LIN_DECAY, true>(p, CL, stream)
-              : launch_fwd_t<PARARNN_LIN_DECAY, false>(p, CL, stream);
+int launch_linrec_fwd(int cell, bool bf16, const LinParams& p, cudaStream_t stream) {
+  if (cell == PARARNN_LIN_GRU)
+    return bf16 ? launch_fwd_t<PARARNN_LIN_GRU, true>(p, stream) : launch_fwd_t<PARARNN_LIN_GRU, false>(p, stream);
+  return bf16 ? launch_fwd_t<PARARNN_LIN_DECAY, true>(p, stream) : launch_fwd_t<PARARNN_LIN_DECAY, false>(p, stream);
 }
 
 int launch_linrec_bwd(int cell, bool bf16, bool bf16_out, LinParams p, float* dlam, float* dbias,
                       cudaStream_t stream) {
-  const int CL = linrec_bwd_cluster(cell, p.B, p.T, p.D);
-  p.ntd = (p.D + kLinTile - 1) / kLinTile;
   if (!dlam && !dbias) p.part = nullptr;
-  int e = cell == PARARNN_LIN_GRU ? launch_bwd_c<PARARNN_LIN_GRU>(bf16, bf16_out, p, CL, stream)
-                                  : launch_bwd_c<PARARNN_LIN_DECAY>(bf16, bf16_out, p, CL, stream);
+  int e = cell == PARARNN_LIN_GRU ? launch_bwd_c<PARARNN_LIN_GRU>(bf16, bf16_out, p, stream)
+                                  : launch_bwd_c<PARARNN_LIN_DECAY>(bf16, bf16_out, p, stream);
   if (e || !p.part) return e;
   const int G = cell == PARARNN_LIN_GRU ? 2 : 3;
   const int C = (G + 1) * p.D;
-  linrec_colsum<<<(C + 31) / 32, 256, 0, stream>>>(p.part, p.B * CL, C, G * p.D, dbias, dlam);
+  linrec_colsum<<<(C + 31) / 32, 256, 0, stream>>>(p.part, p.B * linrec_bwd_cluster(cell, p.B, p.T, p.D), C,
+                                                   G * p.D, dbias, dlam);
   return (int)cudaGetLastError();
 }
 

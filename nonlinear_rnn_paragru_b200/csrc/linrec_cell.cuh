@@ -65,24 +65,19 @@ __device__ __forceinline__ float2 decay_nm(float2 v) {
   return make_float2(v.x < 0.36f ? p.x : e.x, v.y < 0.36f ? p.y : e.y);
 }
 
-// -tanh y and the parts of its derivative 1 - tanh^2 = 4 F R^2, F = e^-2|y|,
-// R = 1 / (1 + F).  Below |y| = 0.3 the Taylor series to y^9 (the next term is
-// below 2^-24 of the sum there), above (1 - F) R with F < 0.55.
-__device__ __forceinline__ float minus_sign_of(float big, float y) {
-  return __uint_as_float(__float_as_uint(big) | (~__float_as_uint(y) & 0x80000000u));
-}
-__device__ __forceinline__ float2 minus_tanh_parts(float2 y, float2& F, float2& R) {
-  F = ex2_neg_abs(lmul(y, both(2.f * kLog2e)));
-  R = rcp_2(ladd(F, both(1.f)));
-  const float2 big = lmul(lfma(F, both(-1.f), both(1.f)), R);
+// -tanh y and R = 1 / (1 + e^2y), of which 1 - tanh^2 = 4 (R - R^2).  Below
+// |y| = 0.2 the Taylor series to y^7 (the next term is below 2^-24 of the sum
+// there); above, 2 R - 1, whose rounding is 2^-23 at most (10 units of the
+// last place of the smallest |tanh| it serves).
+__device__ __forceinline__ float2 minus_tanh(float2 y, float2& R) {
+  R = rcp_2(ladd(ex2_2(lmul(y, both(2.f * kLog2e))), both(1.f)));
+  const float2 big = lfma(R, both(2.f), both(-1.f));
   const float2 s = lmul(y, y);
-  float2 p = lfma(s, both(-62.f / 2835.f), both(17.f / 315.f));
-  p = lfma(s, p, both(-2.f / 15.f));
+  float2 p = lfma(s, both(17.f / 315.f), both(-2.f / 15.f));
   p = lfma(s, p, both(1.f / 3.f));
   p = lfma(s, p, both(-1.f));
   p = lmul(y, p);
-  return make_float2(fabsf(y.x) < 0.3f ? p.x : minus_sign_of(big.x, y.x),
-                     fabsf(y.y) < 0.3f ? p.y : minus_sign_of(big.y, y.y));
+  return make_float2(fabsf(y.x) < 0.2f ? p.x : big.x, fabsf(y.y) < 0.2f ? p.y : big.y);
 }
 
 // log(1 + e^x), once per channel
@@ -112,20 +107,20 @@ struct LinCell<PARARNN_LIN_GRU> {
     return rcp_2(neg2(ladd(ex2_2(zarg(u[0])), both(1.f))));
   }
   __device__ __forceinline__ void coef(const float2 (&u)[G], float2& m, float2& b) const {
-    float2 F, R;
+    float2 R;
     m = nm(u);
-    b = lmul(m, minus_tanh_parts(ladd(u[1], bc), F, R));
+    b = lmul(m, minus_tanh(ladd(u[1], bc), R));
   }
   // du of one step from lambda and h_{t-1}
   __device__ __forceinline__ void grad(const float2 (&u)[G], float2 m, float2 hp, float2 lt, float2 (&du)[G],
                                        float2& /*e*/) const {
-    float2 F, R;
-    const float2 nc = minus_tanh_parts(ladd(u[1], bc), F, R);
+    float2 R;
+    const float2 nc = minus_tanh(ladd(u[1], bc), R);
     const float2 t = ex2_neg_abs(zarg(u[0])), q = rcp_2(ladd(t, both(1.f)));
     const float2 zz = lmul(lmul(t, q), q);  // z (1 - z), where z is near 1 too
     const float2 nl = neg2(lt);
     du[0] = lmul(lmul(nl, ladd(hp, nc)), zz);
-    du[1] = lmul(lmul(nl, m), lmul(lmul(F, both(4.f)), lmul(R, R)));
+    du[1] = lmul(lmul(nl, m), lmul(lfma(neg2(R), R, R), both(4.f)));
   }
   static __device__ __forceinline__ float2 lam_scale(const float*, int) { return both(0.f); }
 };
@@ -227,7 +222,7 @@ struct LinParams {
   float* dh0;
   float* part;           // adjoint: [B * CL][(G + 1) D] sums over a CTA's steps
   int B, T, D;
-  int ntd;               // 64-channel tiles in D
+  int ntd;               // tiles of a batch row (set at the launch)
 };
 
 }  // namespace pararnn

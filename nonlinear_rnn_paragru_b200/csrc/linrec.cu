@@ -19,6 +19,7 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "linrec_cell.cuh"
 
@@ -170,16 +171,18 @@ __device__ __forceinline__ unsigned lin_marks(const unsigned char* at, int dir, 
   return bits;
 }
 
-// Shape of a scan kernel: W warps, K steps of a thread in a round, a ring of S
-// rounds, at least R CTAs on an SM.
+// Shape of a scan kernel: GL lanes of a group, W warps, K steps of a thread in
+// a round, a ring of S rounds, at least R CTAs on an SM.
 template <int CELL, bool kBF16>
 struct FwdShape {
   static constexpr bool kGru = CELL == PARARNN_LIN_GRU;
-#ifdef FW
+#ifdef FG
   static constexpr int GL = FG, W = FW, K = FK, S = FS, R = FR;
 #else
-  static constexpr int GL = 32, W = 4, K = kBF16 && kGru ? 8 : 16, S = kBF16 && kGru ? 3 : 2,
-                       R = kBF16 && kGru ? 5 : kBF16 || kGru ? 3 : 2;
+  static constexpr int GL = 32, W = 4;
+  static constexpr int K = !kBF16 ? 16 : kGru ? 8 : 12;
+  static constexpr int S = kGru ? 3 : 2;
+  static constexpr int R = !kBF16 ? 2 : kGru ? 5 : 4;
 #endif
   using U = Rows<GL, K, LinCell<CELL>::G, kBF16 ? 2 : 4>;
   static constexpr int kWarp = S * U::kRound;   // bytes of a warp's ring
@@ -212,26 +215,31 @@ __global__ void __launch_bounds__(32 * FwdShape<CELL, kBF16>::W, FwdShape<CELL, 
   // copies: this lane's row of an instruction and its piece of the row
   const int crow = lane / U::kLanes, cpiece = lane % U::kLanes;
   const bool cok = dbase + cpiece * U::kPiece < p.D;
-  const char* src = static_cast<const char*>(p.u) + (b * p.sb + dbase + cpiece * U::kPiece) * ES;
   const uint32_t dst = smem_u32(ring) + warp * Shape::kWarp + U::at(crow) + cpiece * 16;
   const char* const mine = ring + warp * Shape::kWarp + U::at(grp * K);
   float4* const cta = reinterpret_cast<float4*>(ring + Shape::kBytes);
   const int round = CL * W * KW, first = (rank * W + warp) * KW;
-  auto copy = [&](int tw, int slot) {  // steps tw .. tw + KW - 1
+  const long long pitch = p.st * ES, gate = p.sg * ES;
+  // this lane's first row of the next round to copy, and the steps from it to
+  // the end of the sequence (none for a lane past D)
+  const char* src =
+      static_cast<const char*>(p.u) + (b * p.sb + dbase + cpiece * U::kPiece) * ES + (first + crow) * pitch;
+  int left = cok ? p.T - first - crow : 0;
+  auto copy = [&](int slot) {
+    const uint32_t to = dst + slot * U::kRound;
 #pragma unroll
-    for (int i = 0; i < U::kCopies; ++i) {
-      const int t = tw + i * U::kRows + crow;
-      if (cok && t < p.T) {
-        const char* s = src + t * (p.st * ES);
-        const uint32_t o = dst + slot * U::kRound + U::at(i * U::kRows);
+    for (int i = 0; i < U::kCopies; ++i)
+      if (i * U::kRows < left) {
 #pragma unroll
-        for (int q = 0; q < G; ++q) cp_async16(o + q * U::kRow, s + q * (p.sg * ES));
+        for (int q = 0; q < G; ++q)
+          cp_async16(to + U::at(i * U::kRows) + q * U::kRow, src + i * (U::kRows * pitch) + q * gate);
       }
-    }
+    src += round * pitch;
+    left -= round;
   };
 #pragma unroll
   for (int s = 0; s < S - 1; ++s) {
-    copy(first + s * round, s);
+    copy(s);
     cp_async_commit();
   }
   Cell cell;
@@ -246,7 +254,7 @@ __global__ void __launch_bounds__(32 * FwdShape<CELL, kBF16>::W, FwdShape<CELL, 
     const int tw = base + first, t0 = tw + grp * K;
     cp_async_wait<S - 2>();
     __syncwarp();
-    copy(tw + (S - 1) * round, slot == 0 ? S - 1 : slot - 1);
+    copy(slot == 0 ? S - 1 : slot - 1);
     cp_async_commit();
     const unsigned resets = kReset ? lin_marks<GL, K>(p.reset + row + t0, 1, p.T - t0) : 0u;
     const char* rows = mine + slot * U::kRound;
@@ -290,11 +298,10 @@ __global__ void __launch_bounds__(32 * FwdShape<CELL, kBF16>::W, FwdShape<CELL, 
 // reset, and mu_1 = dL/dh0).  Positions run from the last step to the first.
 template <int CELL, bool kBF16>
 struct BwdShape {
-  static constexpr bool kGru = CELL == PARARNN_LIN_GRU;
-#ifdef BW
+#ifdef BG
   static constexpr int GL = BG, W = BW, K = BK, S = BS, R = BR;
 #else
-  static constexpr int GL = 32, W = 4, K = 4, S = kBF16 ? 3 : 2, R = 4;
+  static constexpr int GL = 32, W = 4, K = kBF16 ? 12 : 8, S = 2, R = 2;
 #endif
   using U = Rows<GL, K, LinCell<CELL>::G, kBF16 ? 2 : 4>;
   using F = Rows<GL, K, 1, 4>;
@@ -325,43 +332,50 @@ __global__ void __launch_bounds__(32 * BwdShape<CELL, kBF16>::W, BwdShape<CELL, 
   const size_t row = (size_t)b * p.T;
   const int crow = lane / U::kLanes, cpiece = lane % U::kLanes;
   const bool cok = dbase + cpiece * U::kPiece < p.D;
-  const char* src = static_cast<const char*>(p.u) + (b * p.sb + dbase + cpiece * U::kPiece) * ES;
   const int frow = lane / F::kLanes, fpiece = lane % F::kLanes;
   const bool fok = dbase + fpiece * F::kPiece < p.D;
-  const size_t fcol = row * p.D + dbase + fpiece * F::kPiece;
   const uint32_t udst = smem_u32(ring) + warp * Shape::kWarp + U::at(crow) + cpiece * 16;
   const uint32_t fdst = smem_u32(ring) + warp * Shape::kWarp + F::at(frow) + fpiece * 16;
   const char* const umine = ring + warp * Shape::kWarp + U::at(grp * K);
   const char* const fmine = ring + warp * Shape::kWarp + F::at(grp * K);
   float4* const cta = reinterpret_cast<float4*>(ring + Shape::kBytes);
   const int round = CL * W * KW, first = (rank * W + warp) * KW;
-  auto copy = [&](int tw, int slot) {  // steps tw - 1, tw - 2, ..., tw - KW
+  const long long pitch = p.st * ES, gate = p.sg * ES;
+  // this lane's first rows of the next round to copy, and the steps from them
+  // to the first of the sequence; h_{t-1} is a row before dL/dh_t's
+  const char* src = static_cast<const char*>(p.u) + (b * p.sb + dbase + cpiece * U::kPiece) * ES +
+                    (p.T - 1 - first - crow) * pitch;
+  long long fat = ((long long)row + p.T - 1 - first - frow) * p.D + dbase + fpiece * F::kPiece;
+  int uleft = cok ? p.T - first - crow : 0, fleft = fok ? p.T - first - frow : 0;
+  auto copy = [&](int slot) {
+    const uint32_t to = udst + slot * Shape::kRound, fto = fdst + slot * Shape::kRound;
 #pragma unroll
-    for (int i = 0; i < U::kCopies; ++i) {
-      const int t = tw - 1 - i * U::kRows - crow;
-      if (cok && t >= 0) {
-        const char* s = src + t * (p.st * ES);
-        const uint32_t o = udst + slot * Shape::kRound + U::at(i * U::kRows);
+    for (int i = 0; i < U::kCopies; ++i)
+      if (i * U::kRows < uleft) {
 #pragma unroll
-        for (int q = 0; q < G; ++q) cp_async16(o + q * U::kRow, s + q * (p.sg * ES));
+        for (int q = 0; q < G; ++q)
+          cp_async16(to + U::at(i * U::kRows) + q * U::kRow, src - i * (U::kRows * pitch) + q * gate);
       }
-    }
+    const float* g = p.g + fat;
+    const float* h = p.h + fat - p.D;
 #pragma unroll
     for (int i = 0; i < F::kCopies; ++i) {
-      const int t = tw - 1 - i * F::kRows - frow;
-      const uint32_t o = fdst + slot * Shape::kRound + F::at(i * F::kRows);
-      if (fok && t >= 0) cp_async16(o + Shape::kG, p.g + fcol + (size_t)t * p.D);
-      if (fok && t >= 1) cp_async16(o + Shape::kH, p.h + fcol + (size_t)(t - 1) * p.D);
+      const long long o = (long long)i * F::kRows * p.D;
+      if (i * F::kRows < fleft) cp_async16(fto + F::at(i * F::kRows) + Shape::kG, g - o);
+      if (i * F::kRows + 1 < fleft) cp_async16(fto + F::at(i * F::kRows) + Shape::kH, h - o);
     }
+    src -= round * pitch;
+    fat -= (long long)round * p.D;
+    uleft -= round;
+    fleft -= round;
   };
 #pragma unroll
   for (int s = 0; s < S - 1; ++s) {
-    copy(p.T - first - s * round, s);
+    copy(s);
     cp_async_commit();
   }
   Cell cell;
   cell.init(p.lam, p.bias, p.kappa, p.D, d);
-  const float2 h0 = vec2(p.h0 ? p.h0 + (size_t)b * p.D : nullptr, d);
   float2 carry = both(0.f);
   float2 sum[G + 1];
 #pragma unroll
@@ -370,64 +384,75 @@ __global__ void __launch_bounds__(32 * BwdShape<CELL, kBF16>::W, BwdShape<CELL, 
   bool lost = false;
   int slot = 0;
   unsigned nround = 0;
+  using Out = typename std::conditional<kBF16Out, __nv_bfloat162, float2>::type;
+  const size_t pairs = p.D / 2;  // channel pairs of a row of du
+  Out* du_at = static_cast<Out*>(p.du) + ((long long)row + p.T - 1 - first - grp * K) * (long long)(G * pairs) + d / 2;
   for (int end = p.T; end > 0; end -= round, ++nround) {
-    const int tw = end - first, t1 = tw - grp * K;  // this thread's steps: t1 - 1, ..., t1 - K
+    const int t1 = end - first - grp * K;  // this thread's steps: t1 - 1, ..., t1 - K
     cp_async_wait<S - 2>();
     __syncwarp();
-    copy(tw - (S - 1) * round, slot == 0 ? S - 1 : slot - 1);
+    copy(slot == 0 ? S - 1 : slot - 1);
     cp_async_commit();
     const unsigned resets = kReset ? lin_marks<GL, K>(p.reset + row + t1 - 1, -1, t1) : 0u;
     const char* urows = umine + slot * Shape::kRound;
     const char* grows = fmine + slot * Shape::kRound + Shape::kG;
     const char* hrows = fmine + slot * Shape::kRound + Shape::kH;
     slot = slot + 1 == S ? 0 : slot + 1;
-    float2 nm[K], P = both(1.f), Q = both(0.f);
+    // lambda of step j is L[j] + P[j] mu, mu what comes from the steps after
+    float2 nm[K], L[K], P[K], keep[K][Cell::kKeep], mu = both(0.f), pr = both(1.f);
 #pragma unroll
     for (int j = 0; j < K; ++j) {
-      float2 u[G];
-#pragma unroll
-      for (int q = 0; q < G; ++q) u[q] = row_pair<kBF16>(urows + (j * G + q) * U::kRow, gl);
-      nm[j] = cell.nm(u);
-      const float2 lt = ladd(row_pair<false>(grows + j * F::kRow, gl), Q);
-      Q = lfma(nm[j], lt, lt);
-      P = lfma(nm[j], P, P);
-      if (kReset && ((resets >> j) & 1u)) Q = both(0.f);
+      cell.head(row_pair<kBF16>(urows + j * G * U::kRow, gl), nm[j], keep[j]);
+      L[j] = ladd(row_pair<false>(grows + j * F::kRow, gl), mu);
+      P[j] = pr;
+      mu = lfma(nm[j], L[j], L[j]);
+      pr = lfma(nm[j], pr, pr);
+      if (kReset && ((resets >> j) & 1u)) mu = pr = both(0.f);
     }
-    if (kReset && resets) P = both(-1.f);
-    float2 mu = lin_exchange<W, GL, kReset>(sh, cta, nround, make_float4(P.x, P.y, Q.x, Q.y), rank, CL, carry, lost);
+    if (kReset && resets) pr = both(-1.f);
+    mu = lin_exchange<W, GL, kReset>(sh, cta, nround, make_float4(pr.x, pr.y, mu.x, mu.y), rank, CL, carry, lost);
     float2 add[G + 1];
 #pragma unroll
     for (int q = 0; q <= G; ++q) add[q] = both(0.f);
-#pragma unroll
-    for (int j = 0; j < K; ++j) {
-      const int t = t1 - 1 - j;
-      if (t < 0) break;  // steps before the sequence: all that follow too
+    auto step = [&](int j, bool first_step) {
+      float2 lt = lfma(P[j], mu, L[j]);
+      if (kReset && (resets & ((1u << j) - 1u))) lt = L[j];  // nothing of mu comes before a reset
       const bool rs = kReset && ((resets >> j) & 1u);
-      const float2 lt = ladd(row_pair<false>(grows + j * F::kRow, gl), mu);
-      mu = rs ? both(0.f) : lfma(nm[j], lt, lt);
-      float2 hp = t == 0 ? h0 : row_pair<false>(hrows + j * F::kRow, gl);
+      float2 hp = row_pair<false>(hrows + j * F::kRow, gl);
+      if (first_step) {
+        hp = vec2(p.h0 ? p.h0 + (size_t)b * p.D : nullptr, d);
+        if (p.dh0 && live) {
+          const float2 v = rs ? both(0.f) : lfma(nm[j], lt, lt);
+          p.dh0[(size_t)b * p.D + d] = v.x;
+          p.dh0[(size_t)b * p.D + d + 1] = v.y;
+        }
+      }
       if (rs) hp = both(0.f);
       float2 u[G], du[G], e;
 #pragma unroll
-      for (int q = 0; q < G; ++q) u[q] = row_pair<kBF16>(urows + (j * G + q) * U::kRow, gl);
-      cell.grad(u, nm[j], hp, lt, du, e);
-      const size_t at = ((row + t) * G) * p.D + d;
+      for (int q = 1; q < G; ++q) u[q] = row_pair<kBF16>(urows + (j * G + q) * U::kRow, gl);
+      cell.grad(u, nm[j], keep[j], hp, lt, du, e);
+      Out* out = du_at - j * (G * pairs);
 #pragma unroll
       for (int q = 0; q < G; ++q) {
         add[q] = ladd(add[q], du[q]);
         if (!live) continue;
         if constexpr (kBF16Out)
-          *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.du) + at + (size_t)q * p.D) =
-              __float22bfloat162_rn(du[q]);
+          out[q * pairs] = __float22bfloat162_rn(du[q]);
         else
-          *reinterpret_cast<float2*>(static_cast<float*>(p.du) + at + (size_t)q * p.D) = du[q];
+          out[q * pairs] = du[q];
       }
       if (CELL == PARARNN_LIN_DECAY) add[G] = ladd(add[G], e);
-      if (t == 0 && p.dh0 && live) {
-        p.dh0[(size_t)b * p.D + d] = mu.x;
-        p.dh0[(size_t)b * p.D + d + 1] = mu.y;
-      }
+    };
+    if (t1 > K) {
+#pragma unroll
+      for (int j = 0; j < K; ++j) step(j, false);
+    } else {
+#pragma unroll
+      for (int j = 0; j < K; ++j)
+        if (t1 - 1 - j >= 0) step(j, t1 - 1 - j == 0);
     }
+    du_at -= (long long)round * (long long)(G * pairs);
     // a round's sums first, then the running sums: over long sequences the
     // error grows with the number of rounds only
 #pragma unroll

@@ -31,9 +31,9 @@ __device__ __forceinline__ float2 ex2_2(float2 v) { return make_float2(ex2(v.x),
 __device__ __forceinline__ float2 ex2_neg_abs(float2 v) { return make_float2(ex2(-fabsf(v.x)), ex2(-fabsf(v.y))); }
 __device__ __forceinline__ float2 rcp_2(float2 v) { return make_float2(rcp(v.x), rcp(v.y)); }
 __device__ __forceinline__ float2 neg2(float2 v) { return make_float2(-v.x, -v.y); }
-// v < 0 ? a : b, v's sign as of a gate argument times -log2 e
-__device__ __forceinline__ float2 sel_neg(float2 v, float2 a, float2 b) {
-  return make_float2(v.x < 0.f ? a.x : b.x, v.y < 0.f ? a.y : b.y);
+// v > 0 ? a : b
+__device__ __forceinline__ float2 sel_pos(float2 v, float2 a, float2 b) {
+  return make_float2(v.x > 0.f ? a.x : b.x, v.y > 0.f ? a.y : b.y);
 }
 // square root and its reciprocal on the special-function unit (about 1 ulp;
 // 0 and infinity for denormals)
@@ -102,25 +102,26 @@ struct LinCell<PARARNN_LIN_GRU> {
     bc = vec2(bias ? bias + D : nullptr, d);
   }
   __device__ __forceinline__ float2 zarg(float2 u) const { return lfma(u, both(-kLog2e), bz); }
-  // -z = 1 / -(1 + 2^v): 0 where 2^v overflows
-  __device__ __forceinline__ float2 nm(const float2 (&u)[G]) const {
-    return rcp_2(neg2(ladd(ex2_2(zarg(u[0])), both(1.f))));
-  }
-  __device__ __forceinline__ void coef(const float2 (&u)[G], float2& m, float2& b) const {
+  __device__ __forceinline__ void coef(const float2 (&u)[G], float2& nm, float2& b) const {
     float2 R;
-    m = nm(u);
-    b = lmul(m, minus_tanh(ladd(u[1], bc), R));
+    nm = rcp_2(neg2(ladd(ex2_2(zarg(u[0])), both(1.f))));  // -z; 0 where 2^v overflows
+    b = lmul(nm, minus_tanh(ladd(u[1], bc), R));
   }
-  // du of one step from lambda and h_{t-1}
-  __device__ __forceinline__ void grad(const float2 (&u)[G], float2 m, float2 hp, float2 lt, float2 (&du)[G],
-                                       float2& /*e*/) const {
+  // The adjoint's first pass: nm from the first gate, and what the second
+  // keeps of it: z (1 - z), of its own size where z is near 1 too.
+  static constexpr int kKeep = 1;
+  __device__ __forceinline__ void head(float2 u0, float2& nm, float2 (&keep)[kKeep]) const {
+    const float2 v = zarg(u0), t = ex2_neg_abs(v), q = rcp_2(ladd(t, both(1.f))), tq = lmul(t, q);
+    keep[0] = lmul(tq, q);
+    nm = make_float2(v.x > 0.f ? -tq.x : -q.x, v.y > 0.f ? -tq.y : -q.y);
+  }
+  // The second: du of one step from lambda and h_{t-1}.
+  __device__ __forceinline__ void grad(const float2 (&u)[G], float2 nm, const float2 (&keep)[kKeep], float2 hp,
+                                       float2 lt, float2 (&du)[G], float2& /*e*/) const {
     float2 R;
-    const float2 nc = minus_tanh(ladd(u[1], bc), R);
-    const float2 t = ex2_neg_abs(zarg(u[0])), q = rcp_2(ladd(t, both(1.f)));
-    const float2 zz = lmul(lmul(t, q), q);  // z (1 - z), where z is near 1 too
-    const float2 nl = neg2(lt);
-    du[0] = lmul(lmul(nl, ladd(hp, nc)), zz);
-    du[1] = lmul(lmul(nl, m), lmul(lfma(neg2(R), R, R), both(4.f)));
+    const float2 nc = minus_tanh(ladd(u[1], bc), R), nl = neg2(lt);
+    du[0] = lmul(lmul(nl, keep[0]), ladd(hp, nc));
+    du[1] = lmul(lmul(nl, nm), lmul(lfma(neg2(R), R, R), both(4.f)));
   }
   static __device__ __forceinline__ float2 lam_scale(const float*, int) { return both(0.f); }
 };
@@ -135,47 +136,42 @@ struct LinCell<PARARNN_LIN_DECAY> {
     bx = vec2(bias ? bias + 2 * (size_t)D : nullptr, d);
     k = lmul(make_float2(softplus(lam[d]), softplus(lam[d + 1])), both(kappa * kLog2e));
   }
-  // r, i and, over one reciprocal, t = 2^-|arg|, q = 1 / (1 + t) of each
-  __device__ __forceinline__ void gates(const float2 (&u)[G], float2& r, float2& i, float2& tr, float2& qr,
-                                        float2& ti, float2& qi, float2& vr) const {
-    vr = lfma(u[0], both(-kLog2e), br);
-    const float2 vi = lfma(u[1], both(-kLog2e), bi);
-    tr = ex2_neg_abs(vr);
-    ti = ex2_neg_abs(vi);
+  __device__ __forceinline__ void coef(const float2 (&u)[G], float2& nm, float2& b) const {
+    // r and i over one reciprocal: sig(x) is q = 1 / (1 + 2^-|v|) for x >= 0
+    // (v <= 0), 2^-|v| q below
+    const float2 vr = lfma(u[0], both(-kLog2e), br), vi = lfma(u[1], both(-kLog2e), bi);
+    const float2 tr = ex2_neg_abs(vr), ti = ex2_neg_abs(vi);
     const float2 dr = ladd(tr, both(1.f)), di = ladd(ti, both(1.f)), inv = rcp_2(lmul(dr, di));
-    qr = lmul(di, inv);
-    qi = lmul(dr, inv);
-    // sig(x) is q for x >= 0 (v <= 0), t q below
-    r = lmul(sel_neg(neg2(vr), tr, both(1.f)), qr);
-    i = lmul(sel_neg(neg2(vi), ti, both(1.f)), qi);
-  }
-  __device__ __forceinline__ float2 nm(const float2 (&u)[G]) const {
-    const float2 r = rcp_2(ladd(ex2_2(lfma(u[0], both(-kLog2e), br)), both(1.f)));
-    return decay_nm(lmul(k, r));
-  }
-  __device__ __forceinline__ void coef(const float2 (&u)[G], float2& m, float2& b) const {
-    float2 r, i, tr, qr, ti, qi, vr;
-    gates(u, r, i, tr, qr, ti, qi, vr);
-    m = decay_nm(lmul(k, r));
-    const float2 s = lmul(m, ladd(m, both(2.f)));  // -(1 - a^2)
+    const float2 r = lmul(sel_pos(vr, tr, both(1.f)), lmul(di, inv));
+    const float2 i = lmul(sel_pos(vi, ti, both(1.f)), lmul(dr, inv));
+    nm = decay_nm(lmul(k, r));
+    const float2 s = lmul(nm, ladd(nm, both(2.f)));  // -(1 - a^2)
     b = lmul(lmul(make_float2(sqrt_apx(-s.x), sqrt_apx(-s.y)), i), ladd(u[2], bx));
   }
-  __device__ __forceinline__ void grad(const float2 (&u)[G], float2 m, float2 hp, float2 lt, float2 (&du)[G],
-                                       float2& e) const {
-    float2 r, i, tr, qr, ti, qi, vr;
-    gates(u, r, i, tr, qr, ti, qi, vr);
-    const float2 x = ladd(u[2], bx), a = ladd(m, both(1.f)), w = lmul(lmul(k, r), both(kLn2));
-    const float2 s = lmul(neg2(m), ladd(m, both(2.f)));  // beta^2
+  // kept for the second pass: w = -log a and 1 - r
+  static constexpr int kKeep = 2;
+  __device__ __forceinline__ void head(float2 u0, float2& nm, float2 (&keep)[kKeep]) const {
+    const float2 v = lfma(u0, both(-kLog2e), br), t = ex2_neg_abs(v), q = rcp_2(ladd(t, both(1.f)));
+    const float2 tq = lmul(t, q), w = lmul(k, sel_pos(v, tq, q));
+    nm = decay_nm(w);
+    keep[0] = lmul(w, both(kLn2));
+    keep[1] = sel_pos(v, q, tq);
+  }
+  __device__ __forceinline__ void grad(const float2 (&u)[G], float2 nm, const float2 (&keep)[kKeep], float2 hp,
+                                       float2 lt, float2 (&du)[G], float2& e) const {
+    const float2 v = lfma(u[1], both(-kLog2e), bi), t = ex2_neg_abs(v), q = rcp_2(ladd(t, both(1.f)));
+    const float2 tq = lmul(t, q), i = sel_pos(v, tq, q);
+    const float2 x = ladd(u[2], bx), a = ladd(nm, both(1.f)), w = keep[0];
+    const float2 s = lmul(neg2(nm), ladd(nm, both(2.f)));  // beta^2
     // 1 / beta; w / beta -> 0 with w
     const float2 rb = make_float2(s.x >= 1.1754944e-38f ? rsqrt_apx(s.x) : 0.f,
                                   s.y >= 1.1754944e-38f ? rsqrt_apx(s.y) : 0.f);
-    const float2 beta = lmul(s, rb);
     // r dL/dr = lambda (a^2 i x w / beta - a h_{t-1} w):  d beta = (a^2 / beta) dw
-    const float2 ix = lmul(i, x);
-    e = lmul(lmul(lt, a), lfma(lmul(a, ix), lmul(w, rb), neg2(lmul(hp, w))));
-    du[0] = lmul(e, lmul(sel_neg(neg2(vr), both(1.f), tr), qr));
-    const float2 lb = lmul(lt, beta);
-    du[1] = lmul(lmul(lb, x), lmul(lmul(ti, qi), qi));
+    const float2 lw = lmul(lmul(lt, a), w);
+    e = lmul(lw, lfma(lmul(a, rb), lmul(i, x), neg2(hp)));
+    du[0] = lmul(e, keep[1]);
+    const float2 lb = lmul(lt, lmul(s, rb));
+    du[1] = lmul(lmul(lb, x), lmul(tq, q));
     du[2] = lmul(lb, i);
   }
   static __device__ __forceinline__ float2 lam_scale(const float* lam, int d) {

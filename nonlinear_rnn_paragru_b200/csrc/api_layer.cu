@@ -85,9 +85,7 @@ NormParams norm_params(const void* h, int h_dtype, long long ld_h, const void* g
   p.ld_h = ld_h;
   p.ld_g = ld_g;
   p.ld_r = ld_r;
-  p.h32 = h_dtype == PARARNN_F32;
-  p.g32 = g_dtype == PARARNN_F32;
-  p.r32 = r_dtype == PARARNN_F32;
+  p.types = (h_dtype == PARARNN_F32 ? 1 : 0) | (g_dtype == PARARNN_F32 ? 2 : 0) | (r_dtype == PARARNN_F32 ? 4 : 0);
   p.w_post = w_post;
   p.scale = scale;
   p.w_pre = w_pre;
@@ -174,8 +172,7 @@ int pararnn_block_norm(const void* h, int h_dtype, long long h_stride, const voi
                              res_stride, scale, w_pre, eps, N, D);
   p.s = s;
   p.x = x;
-  p.s32 = s_dtype == PARARNN_F32;
-  p.x32 = x_dtype == PARARNN_F32;
+  p.types |= (s_dtype == PARARNN_F32 ? 8 : 0) | (x_dtype == PARARNN_F32 ? 16 : 0);
   return done(launch_norm_fwd(p, (cudaStream_t)stream));
 }
 
@@ -211,8 +208,7 @@ int pararnn_block_norm_adjoint(const void* h, int h_dtype, long long h_stride, c
   p.dx = dx;
   p.ld_ds = ds_stride;
   p.ld_dx = dx_stride;
-  p.ds32 = ds_dtype == PARARNN_F32;
-  p.dx32 = dx_dtype == PARARNN_F32;
+  p.types |= (ds_dtype == PARARNN_F32 ? 8 : 0) | (dx_dtype == PARARNN_F32 ? 16 : 0);
   p.dh = dh;
   p.dg = dgate;
   p.dres = dres;

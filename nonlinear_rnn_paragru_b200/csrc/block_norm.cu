@@ -4,337 +4,522 @@
 //   s = res + scale y                      x = s rsqrt(mean s^2 + eps) w_pre
 // A row stays in the registers of the threads that own it from its first read
 // to its last write, so each input is read once and each output written once;
-// sums over the row and all arithmetic are fp32, each output is rounded once.
+// sums over the row and all arithmetic are fp32 (two channels an instruction),
+// each output is rounded once.
+//
+// Blocks walk over rows: `tpr` threads a row of 8 NV channels each (a power of
+// two up to a warp for D <= 256, several rows a block; else the whole block),
+// and a thread loads its share of the next row before it works on this one, so
+// that HBM stays busy through the row's two or three sums.
 #include <algorithm>
+#include <utility>
 
 #include "block_norm.cuh"
 #include "linrec_cell.cuh"
 
 namespace pararnn {
-
 namespace {
+
+// Types of the tensors: a kernel for every combination in common use, with
+// the types known to the compiler, and one (kAnyType) that looks at the
+// parameters.  Bits: h, gate, res, s (or ds), x (or dx) are fp32.
+constexpr int kH32 = 1, kG32 = 2, kR32 = 4, kS32 = 8, kX32 = 16, kAnyType = -1;
+template <int TP>
+__device__ __forceinline__ bool f32(const NormParams& p, int bit) {
+  return ((TP == kAnyType ? p.types : TP) & bit) != 0;
+}
+
+// Parts that a call has, alike: known to the compiler for those in common use.
+constexpr int kPost = 1, kGate = 2, kRes = 4, kScale = 8, kPre = 16, kDs = 32, kAnyPart = -1;
+template <int PT>
+__device__ __forceinline__ bool has(const NormParams& p, int bit) {
+  return ((PT == kAnyPart ? p.parts : PT) & bit) != 0;
+}
 
 // 8 channels of a row as they lie in memory: 16 bytes of bf16 or 32 of fp32.
 struct Raw8 {
   uint4 a, b;
 };
-__device__ __forceinline__ Raw8 raw_zero() { return {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}; }
-__device__ __forceinline__ Raw8 raw_load(const void* p, long long i, bool f32) {
-  Raw8 r = raw_zero();
+__device__ __forceinline__ Raw8 raw_load(const void* p, long long i, bool f32, bool ok) {
+  Raw8 r = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
   const uint4* q = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + i * (f32 ? 4 : 2));
-  r.a = q[0];
-  if (f32) r.b = q[1];
+  if (ok) r.a = q[0];
+  if (ok && f32) r.b = q[1];
   return r;
 }
-__device__ __forceinline__ void raw_get(const Raw8& r, bool f32, float (&v)[8]) {
-  const unsigned w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 t = bf16_pair(w[i]);
-    v[2 * i] = f32 ? __uint_as_float(w[2 * i]) : t.x;
-    v[2 * i + 1] = f32 ? __uint_as_float(w[2 * i + 1]) : t.y;
-  }
+struct F8 {
+  float2 v[4];
+};
+__device__ __forceinline__ float2 bits2(unsigned x, unsigned y) {
+  return make_float2(__uint_as_float(x), __uint_as_float(y));
 }
-__device__ __forceinline__ unsigned pack2(float a, float b) {
-  const __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
+__device__ __forceinline__ F8 raw_get(const Raw8& r, bool f32) {
+  if (f32) return {bits2(r.a.x, r.a.y), bits2(r.a.z, r.a.w), bits2(r.b.x, r.b.y), bits2(r.b.z, r.b.w)};
+  return {bf16_pair(r.a.x), bf16_pair(r.a.y), bf16_pair(r.a.z), bf16_pair(r.a.w)};
+}
+__device__ __forceinline__ unsigned pack2(float2 v) {
+  const __nv_bfloat162 t = __float22bfloat162_rn(v);
   return *reinterpret_cast<const unsigned*>(&t);
 }
-__device__ __forceinline__ void store8(void* p, long long i, bool f32, const float (&v)[8]) {
+__device__ __forceinline__ void store8(void* p, long long i, bool f32, const F8& x) {
   if (f32) {
     float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
-    q[0] = make_float4(v[0], v[1], v[2], v[3]);
-    q[1] = make_float4(v[4], v[5], v[6], v[7]);
+    q[0] = make_float4(x.v[0].x, x.v[0].y, x.v[1].x, x.v[1].y);
+    q[1] = make_float4(x.v[2].x, x.v[2].y, x.v[3].x, x.v[3].y);
   } else {
     *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p) + i) =
-        make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+        make_uint4(pack2(x.v[0]), pack2(x.v[1]), pack2(x.v[2]), pack2(x.v[3]));
   }
 }
-__device__ __forceinline__ void vec8(const float* w, int c, float (&v)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(w + c));
-  const float4 b = __ldg(reinterpret_cast<const float4*>(w + c) + 1);
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-  v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+// 8 weights from channel c on; ones where there are none
+__device__ __forceinline__ F8 weights(const float* w, int c, bool ok) {
+  F8 r = {both(1.f), both(1.f), both(1.f), both(1.f)};
+  if (w && ok) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(w + c));
+    const float4 b = __ldg(reinterpret_cast<const float4*>(w + c) + 1);
+    r = {make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)};
+  }
+  return r;
 }
 
-// sig(g) and its complement
-__device__ __forceinline__ void sig2(float g, float& q, float& qc) {
-  const float t = ex2(-kLog2e * fabsf(g)), pos = rcp(1.f + t), neg = t * pos;
-  q = g >= 0.f ? pos : neg;
-  qc = g >= 0.f ? neg : pos;
-}
-__device__ __forceinline__ float act(int kind, float g) {
-  float q, qc;
-  sig2(g, q, qc);
-  return kind == PARARNN_ACT_SILU ? g * q : q;
-}
-__device__ __forceinline__ void act_grad(int kind, float g, float& v, float& dv) {
-  float q, qc;
-  sig2(g, q, qc);
-  v = kind == PARARNN_ACT_SILU ? g * q : q;
-  dv = kind == PARARNN_ACT_SILU ? q * fmaf(g, qc, 1.f) : q * qc;
-}
+// The gate: act(g) = f s with s = sig(g) and f = g (silu) or 1.
+struct Act {
+  bool silu;
+  __device__ __forceinline__ float2 factor(float2 g) const { return silu ? g : both(1.f); }
+  __device__ __forceinline__ float2 operator()(float2 g) const {
+    return lmul(factor(g), rcp_2(ladd(ex2_2(lmul(g, both(-kLog2e))), both(1.f))));
+  }
+  // and act'(g) = f s (1 - s) (+ s for silu), 1 - s = t s of its own size where
+  // s is near 1 too (t = e^-g, kept finite: s is 0 where it overflows)
+  __device__ __forceinline__ void grad(float2 g, float2& a, float2& da) const {
+    const float2 t = ex2_2(lmul(g, both(-kLog2e))), s = rcp_2(ladd(t, both(1.f))), f = factor(g);
+    const float2 ts = lmul(finite(t), s);
+    a = lmul(f, s);
+    da = lfma(a, ts, silu ? s : both(0.f));
+  }
+};
 
-constexpr int kNormMaxWarps = 32;
+constexpr int kNormWarps = 16;  // of a block, at most
+struct NormShared {
+  float red[2][2][kNormWarps];
+};
+// entries of warps that a block does not have stay zero
+__device__ __forceinline__ void norm_start(NormShared& sh) {
+  if (threadIdx.x < 4 * kNormWarps) (&sh.red[0][0][0])[threadIdx.x] = 0.f;
+  __syncthreads();
+}
 
 // Sums over the threads of a row, the same in every thread of it: shuffles in
-// a warp, then the warps' sums in warp order.  `buf` alternates between two
-// buffers from call to call, so one barrier a call is enough.
+// a warp, then over the warps' sums.  `buf` alternates from call to call, so
+// one barrier a call is enough.
 template <int NVAL>
-__device__ __forceinline__ void row_sum(float (&v)[NVAL], int warps, float (*red)[kNormMaxWarps][2], int& buf) {
+__device__ __forceinline__ void row_sum(float (&v)[NVAL], int tpr, NormShared& sh, int& buf) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
+    if (o < tpr)
 #pragma unroll
-    for (int i = 0; i < NVAL; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-  if (warps == 1) return;
-  if ((threadIdx.x & 31) == 0)
+      for (int i = 0; i < NVAL; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+  if (tpr <= 32) return;
+  const int lane = threadIdx.x & 31;
+  if (lane == 0)
 #pragma unroll
-    for (int i = 0; i < NVAL; ++i) red[buf][threadIdx.x >> 5][i] = v[i];
+    for (int i = 0; i < NVAL; ++i) sh.red[buf][i][threadIdx.x >> 5] = v[i];
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < NVAL; ++i) {
-    v[i] = 0.f;
-    for (int w = 0; w < warps; ++w) v[i] += red[buf][w][i];
+  for (int i = 0; i < NVAL; ++i) v[i] = sh.red[buf][i][lane & (kNormWarps - 1)];
+#pragma unroll
+  for (int o = kNormWarps / 2; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < NVAL; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+  buf ^= 1;
+}
+// The same for six sums at once.  A warp's two halves take three of them each
+// after the first exchange, so 30 shuffles do what 54 would.
+struct NormShared6 {
+  float red[2][6][kNormWarps];
+};
+template <bool kNarrow>
+__device__ __forceinline__ void row_sum6(float (&v)[6], int tpr, NormShared6& sh, int& buf) {
+  if (kNarrow) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      if (o < tpr)
+#pragma unroll
+        for (int i = 0; i < 6; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    return;
+  }
+  const int lane = threadIdx.x & 31, w = lane & (kNormWarps - 1);
+  const bool high = lane >= 16;
+  float h[3];
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const float give = high ? v[i] : v[i + 3];
+    h[i] = (high ? v[i + 3] : v[i]) + __shfl_xor_sync(0xffffffffu, give, 16);
+  }
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < 3; ++i) h[i] += __shfl_xor_sync(0xffffffffu, h[i], o);
+  float(*red)[kNormWarps] = sh.red[buf] + (high ? 3 : 0);
+  if (w == 0)
+#pragma unroll
+    for (int i = 0; i < 3; ++i) red[i][threadIdx.x >> 5] = h[i];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 3; ++i) h[i] = red[i][w];
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < 3; ++i) h[i] += __shfl_xor_sync(0xffffffffu, h[i], o);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const float other = __shfl_xor_sync(0xffffffffu, h[i], 16);
+    v[i] = high ? other : h[i];
+    v[i + 3] = high ? h[i] : other;
   }
   buf ^= 1;
 }
+__device__ __forceinline__ float dot8(const F8& a, const F8& b, float acc) {
+  float2 q = make_float2(acc, 0.f);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) q = lfma(a.v[j], b.v[j], q);
+  return q.x + q.y;
+}
 
-// tpr threads a row (a warp, or the whole block), NV x 8 channels a thread.
 template <int NV>
+struct FwdRow {
+  Raw8 h[NV], g[NV], r[NV];
+};
+
+template <int NV, int TP>
 __global__ void __launch_bounds__(512) norm_fwd(const NormParams p, const int tpr) {
-  __shared__ float red[2][kNormMaxWarps][2];
-  const int slot = threadIdx.x / tpr, t = threadIdx.x - slot * tpr, warps = tpr / 32;
-  const long long row = (long long)blockIdx.x * (blockDim.x / tpr) + slot;
-  if (row >= p.N) return;  // whole warps; blocks of one row never leave here
-  int buf = 0;
+  __shared__ __align__(16) NormShared sh;
+  const int slots = blockDim.x / tpr, slot = threadIdx.x / tpr, t = threadIdx.x % tpr;
+  const long long step = (long long)gridDim.x * slots;
   const float invD = 1.f / (float)p.D;
-  Raw8 rh[NV], rg[NV], rr[NV];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = 8 * (i * tpr + t);
-    rh[i] = rg[i] = rr[i] = raw_zero();
-    if (c < p.D) {
-      rh[i] = raw_load(p.h, row * p.ld_h + c, p.h32);
-      if (p.g) rg[i] = raw_load(p.g, row * p.ld_g + c, p.g32);
-      if (p.res) rr[i] = raw_load(p.res, row * p.ld_r + c, p.r32);
-    }
-  }
-  float y[NV][8];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) raw_get(rh[i], p.h32, y[i]);
-  if (p.w_post) {
-    float q[1] = {0.f};
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) q[0] = fmaf(y[i][j], y[i][j], q[0]);
-    row_sum(q, warps, red, buf);
-    const float k = rsqrtf(fmaf(q[0], invD, p.eps));
+  const Act act = {p.act == PARARNN_ACT_SILU};
+  int buf = 0;
+  norm_start(sh);
+  auto load = [&](long long row, FwdRow<NV>& x) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = 8 * (i * tpr + t);
-      if (c < p.D) {
-        float w[8];
-        vec8(p.w_post, c, w);
+      const bool ok = c < p.D && row < p.N;
+      x.h[i] = raw_load(p.h, row * p.ld_h + c, f32<TP>(p, kH32), ok);
+      x.g[i] = raw_load(p.g, row * p.ld_g + c, f32<TP>(p, kG32), ok && p.g);
+      x.r[i] = raw_load(p.res, row * p.ld_r + c, f32<TP>(p, kR32), ok && p.res);
+    }
+  };
+  FwdRow<NV> cur, nxt;
+  long long row = (long long)blockIdx.x * slots + slot;
+  load(row, cur);
+  // every thread of a block makes the same rounds; rows past N hold zeros
+  for (long long r0 = (long long)blockIdx.x * slots; r0 < p.N; r0 += step, row += step) {
+    load(row + step, nxt);
+    F8 y[NV];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[i][j] = y[i][j] * k * w[j];
+    for (int i = 0; i < NV; ++i) y[i] = raw_get(cur.h[i], f32<TP>(p, kH32));
+    float2 k = both(1.f);
+    if (p.w_post) {
+      float q[1] = {0.f};
+#pragma unroll
+      for (int i = 0; i < NV; ++i) q[0] = dot8(y[i], y[i], q[0]);
+      row_sum(q, tpr, sh, buf);
+      k = both(rsqrtf(fmaf(q[0], invD, p.eps)));
+    }
+    float q[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = 8 * (i * tpr + t);
+      const bool ok = c < p.D && row < p.N;
+      if (p.w_post) {
+        const F8 w = weights(p.w_post, c, ok);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[i].v[j] = lmul(lmul(y[i].v[j], k), w.v[j]);
+      }
+      if (p.g) {
+        const F8 g = raw_get(cur.g[i], f32<TP>(p, kG32));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[i].v[j] = lmul(y[i].v[j], act(g.v[j]));
+      }
+      const F8 r = raw_get(cur.r[i], f32<TP>(p, kR32)), sc = weights(p.scale, c, ok);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[i].v[j] = lfma(y[i].v[j], sc.v[j], r.v[j]);
+      if (p.s && ok) store8(p.s, row * p.D + c, f32<TP>(p, kS32), y[i]);
+      q[0] = dot8(y[i], y[i], q[0]);
+    }
+    if (p.w_pre) {
+      row_sum(q, tpr, sh, buf);
+      const float2 ks = both(rsqrtf(fmaf(q[0], invD, p.eps)));
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = 8 * (i * tpr + t);
+        const bool ok = c < p.D && row < p.N;
+        const F8 w = weights(p.w_pre, c, ok);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[i].v[j] = lmul(lmul(y[i].v[j], ks), w.v[j]);
+        if (ok) store8(p.x, row * p.D + c, f32<TP>(p, kX32), y[i]);
       }
     }
-  }
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = 8 * (i * tpr + t);
-    if (c >= p.D) continue;
-    float v[8];
-    if (p.g) {
-      raw_get(rg[i], p.g32, v);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y[i][j] *= act(p.act, v[j]);
-    }
-    if (p.scale) {
-      vec8(p.scale, c, v);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y[i][j] *= v[j];
-    }
-    if (p.res) {
-      raw_get(rr[i], p.r32, v);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y[i][j] += v[j];
-    }
-    if (p.s) store8(p.s, row * p.D + c, p.s32, y[i]);
-  }
-  if (!p.w_pre) return;
-  float q[1] = {0.f};
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) q[0] = fmaf(y[i][j], y[i][j], q[0]);  // 0 past D
-  row_sum(q, warps, red, buf);
-  const float k = rsqrtf(fmaf(q[0], invD, p.eps));
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = 8 * (i * tpr + t);
-    if (c >= p.D) continue;
-    float w[8];
-    vec8(p.w_pre, c, w);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) y[i][j] = y[i][j] * k * w[j];
-    store8(p.x, row * p.D + c, p.x32, y[i]);
+    cur = nxt;
   }
 }
 
-// Adjoint.  Blocks walk over rows; the sums for the [D] weights stay in
-// registers and leave once per block.  With sh = s / rms(s), hh = h / rms(h):
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// One tensor of the adjoint's ring: this thread's channels of the next row to
+// copy, the bytes from a row to the thread's next, and where they lie in a
+// slot (16-byte pieces, the threads' side by side; `second`: from the first
+// piece of 8 fp32 channels to the other).
+struct RingTensor {
+  const char* at;
+  long long step;
+  int offset;
+};
+
+// Adjoint.  With sh = s / rms(s), hh = h / rms(h):
 //   d = ds + (dx w_pre - sh mean(dx w_pre sh)) / rms(s)      (= dres)
 //   dw_pre = sum dx sh,  dscale = sum d y,  d' = d scale,  dg = d' n act'(g)
 //   d'' = d' act(g),  dw_post = sum d'' hh
 //   dh = (d'' w_post - hh mean(d'' w_post hh)) / rms(h)
-template <int NV>
-__global__ void __launch_bounds__(512) norm_bwd(const NormParams p, const int tpr) {
-  __shared__ float red[2][kNormMaxWarps][2];
-  const int slots = blockDim.x / tpr;
-  const int slot = threadIdx.x / tpr, t = threadIdx.x - slot * tpr, warps = tpr / 32;
-  int buf = 0;
+// d'' w_post hh is d z with z = scale y, and d is linear in what the second
+// norm's sums give, so one exchange serves a row: sums of s^2, s e, ds z, e z
+// and s z (e = dx w_pre), and of the next row's h^2.
+//
+// Every thread copies its own channels of its rows to come into a ring of `S`
+// rows in shared memory (cp.async) and reads them from there where it needs
+// them: five tensors of a row and a row ahead do not fit beside the weights and
+// their sums in the registers.  The sums leave once per block.
+template <int NV, bool kNarrow, int TP, int PT>
+__global__ void __launch_bounds__(512) norm_bwd(const NormParams p, const int tpr, const int S) {
+  extern __shared__ __align__(16) char smem[];
+  __shared__ __align__(16) NormShared6 sh;
+  // kNarrow: rows of a warp at most, several a block; else a row is the block's
+  const int threads = blockDim.x, slots = kNarrow ? threads / tpr : 1, slot = kNarrow ? threadIdx.x / tpr : 0;
+  const int t = kNarrow ? threadIdx.x % tpr : threadIdx.x;
+  const int piece = 16 * threads;
+  const long long step = (long long)gridDim.x * slots;
   const float invD = 1.f / (float)p.D;
-  float aw[NV][8], as[NV][8], ap[NV][8];
+  const Act act = {p.act == PARARNN_ACT_SILU};
+  int buf = 0;
+  long long row = (long long)blockIdx.x * slots + slot;
+  int bytes = 0;  // of a slot of the ring
+  const bool post = has<PT>(p, kPost), gate = has<PT>(p, kGate), pre = has<PT>(p, kPre),
+             res = has<PT>(p, kRes), sum = has<PT>(p, kRes) && pre, scale = has<PT>(p, kScale), dsum = has<PT>(p, kDs);
+  auto tensor = [&](const void* q, long long ld, int bit, bool on) {
+    const int es = f32<TP>(p, bit) ? 4 : 2;
+    RingTensor r = {static_cast<const char*>(q) + (row * ld + 8 * t) * es, step * ld * es, bytes};
+    if (on) bytes += NV * (es / 2) * piece;
+    return r;
+  };
+  RingTensor th = tensor(p.h, p.ld_h, kH32, true), tg = tensor(p.g, p.ld_g, kG32, gate),
+             tr = tensor(p.res, p.ld_r, kR32, sum), ts = tensor(p.ds, p.ld_ds, kS32, dsum),
+             tx = tensor(p.dx, p.ld_dx, kX32, pre);
+  // a thread with channels past D starts from zeros and never copies those
+  if (8 * ((NV - 1) * tpr + t) >= p.D)
+    for (int i = threadIdx.x * 16; i < S * bytes; i += piece)
+      *reinterpret_cast<uint4*>(smem + i) = make_uint4(0, 0, 0, 0);
+  if (threadIdx.x < kNormWarps)
+    for (int i = 0; i < 12; ++i) (&sh.red[0][0][0])[i * kNormWarps + threadIdx.x] = 0.f;
+  __syncthreads();
+  F8 wreg[3];  // of one vector; two vectors a thread read them again for each row
+  if (NV == 1) {
+    wreg[0] = weights(p.w_post, 8 * t, 8 * t < p.D);
+    wreg[1] = weights(p.scale, 8 * t, 8 * t < p.D);
+    wreg[2] = weights(p.w_pre, 8 * t, 8 * t < p.D);
+  }
+  auto weight = [&](int k, int i) {
+    if (NV == 1) return wreg[k];
+    const int c = 8 * (i * tpr + t);
+    return weights(k == 0 ? p.w_post : k == 1 ? p.scale : p.w_pre, c, c < p.D);
+  };
+  const uint32_t base = smem_u32(smem);
+  // past N nothing is copied; where a block has several rows, the last ones of
+  // its last round become zeros
+  auto copy1 = [&](RingTensor& r, int bit, bool in, int k) {
+    const bool wide = f32<TP>(p, bit);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (8 * (i * tpr + t) >= p.D) continue;
+      const char* q = r.at + i * (8 * tpr * (wide ? 4 : 2));
+      const int to = 16 * threadIdx.x + k * bytes + r.offset + i * piece;
+      if (in) {
+        copy16(base + to, q);
+        if (wide) copy16(base + to + NV * piece, q + 16);
+      } else if (kNarrow) {
+        *reinterpret_cast<uint4*>(smem + to) = make_uint4(0, 0, 0, 0);
+        if (wide) *reinterpret_cast<uint4*>(smem + to + NV * piece) = make_uint4(0, 0, 0, 0);
+      }
+    }
+    r.at += r.step;
+  };
+  auto copy = [&](long long row, int k) {  // the next row, into slot k
+    copy1(th, kH32, row < p.N, k);
+    if (gate) copy1(tg, kG32, row < p.N, k);
+    if (sum) copy1(tr, kR32, row < p.N, k);
+    if (dsum) copy1(ts, kS32, row < p.N, k);
+    if (pre) copy1(tx, kX32, row < p.N, k);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto get = [&](const RingTensor& r, int bit, int i, int k, bool on = true) {
+    if (!on) return F8{both(0.f), both(0.f), both(0.f), both(0.f)};
+    const char* q = smem + 16 * threadIdx.x + k * bytes + r.offset + i * piece;
+    Raw8 v;
+    v.a = *reinterpret_cast<const uint4*>(q);
+    v.b = f32<TP>(p, bit) ? *reinterpret_cast<const uint4*>(q + NV * piece) : v.a;
+    return raw_get(v, f32<TP>(p, bit));
+  };
+  // all but the `S - 2` latest copies are there: this row's and the next one's
+  auto wait = [&]() {
+    if (S == 4)
+      asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else if (S == 3)
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+  };
+  auto squares = [&](int k) {
+    float q = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const F8 h = get(th, kH32, i, k);
+      q = dot8(h, h, q);
+    }
+    return q;
+  };
+  F8 aw[NV], as[NV], ap[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) aw[i][j] = as[i][j] = ap[i][j] = 0.f;
-  for (long long row = (long long)blockIdx.x * slots + slot; row < p.N; row += (long long)gridDim.x * slots) {
-    Raw8 rh[NV], rg[NV], rr[NV], rs[NV], rx[NV];
+    for (int j = 0; j < 4; ++j) aw[i].v[j] = as[i].v[j] = ap[i].v[j] = both(0.f);
+  for (int k = 0; k < S - 1; ++k) copy(row + k * step, k);
+  float kh1 = 1.f;  // 1 / rms(h) of the row at hand
+  auto first_norm = [&]() {
+    wait();
+    float q[6] = {squares(0), 0.f, 0.f, 0.f, 0.f, 0.f};
+    row_sum6<kNarrow>(q, tpr, sh, buf);
+    kh1 = rsqrtf(fmaf(q[0], invD, p.eps));
+  };
+  if (post && S > 1) first_norm();
+  int at = 0;  // slot of the row at hand
+  for (long long r0 = (long long)blockIdx.x * slots; r0 < p.N; r0 += step, row += step) {
+    copy(row + (S - 1) * step, at == 0 ? S - 1 : at - 1);
+    const int next = at + 1 == S ? 0 : at + 1;
+    if (S == 1 && post) first_norm();  // a ring of one row: nothing is ahead
+    wait();
+    const float2 kh = both(kh1);
+    float q[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    F8 hh[NV], s[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      hh[i] = get(th, kH32, i, at);
+      const F8 wp = weight(0, i), sc = weight(1, i), w = weight(2, i);
+      F8 z, e = get(tx, kX32, i, at, pre);
+      const F8 g = get(tg, kG32, i, at, gate), ds = get(ts, kS32, i, at, dsum),
+               r = get(tr, kR32, i, at, sum);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        z.v[j] = hh[i].v[j];
+        if (post) z.v[j] = hh[i].v[j] = lmul(z.v[j], kh), z.v[j] = lmul(z.v[j], wp.v[j]);
+        if (scale) z.v[j] = lmul(z.v[j], sc.v[j]);
+        if (gate) z.v[j] = lmul(z.v[j], act(g.v[j]));
+        s[i].v[j] = sum ? ladd(r.v[j], z.v[j]) : z.v[j];
+        e.v[j] = lmul(e.v[j], w.v[j]);
+      }
+      if (pre) {
+        q[0] = dot8(s[i], s[i], q[0]);
+        q[1] = dot8(s[i], e, q[1]);
+      }
+      if (post && dsum) q[2] = dot8(ds, z, q[2]);
+      if (post && pre) {
+        q[3] = dot8(e, z, q[3]);
+        q[4] = dot8(s[i], z, q[4]);
+      }
+    }
+    if (post) q[5] = squares(next);
+    row_sum6<kNarrow>(q, tpr, sh, buf);
+    const float k1 = pre ? rsqrtf(fmaf(q[0], invD, p.eps)) : 0.f, nm1 = -(q[1] * k1 * invD);
+    const float2 k = both(k1), nmean = both(nm1);
+    const float2 nmean3 = both(-(fmaf(k1, fmaf(k1 * nm1, q[4], q[3]), q[2]) * invD));
+    if (post) kh1 = rsqrtf(fmaf(q[5], invD, p.eps));
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = 8 * (i * tpr + t);
-      rh[i] = rg[i] = rr[i] = rs[i] = rx[i] = raw_zero();
-      if (c < p.D) {
-        rh[i] = raw_load(p.h, row * p.ld_h + c, p.h32);
-        if (p.g) rg[i] = raw_load(p.g, row * p.ld_g + c, p.g32);
-        if (p.res && p.w_pre) rr[i] = raw_load(p.res, row * p.ld_r + c, p.r32);
-        if (p.ds) rs[i] = raw_load(p.ds, row * p.ld_ds + c, p.ds32);
-        if (p.w_pre) rx[i] = raw_load(p.dx, row * p.ld_dx + c, p.dx32);
+      const bool ok = c < p.D && row < p.N;
+      const F8 wp = weight(0, i), sc = weight(1, i), w = weight(2, i);
+      F8 d = get(ts, kS32, i, at, dsum);
+      const F8 dx = get(tx, kX32, i, at, pre);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (!pre) continue;
+        const float2 sn = lmul(s[i].v[j], k);
+        ap[i].v[j] = lfma(dx.v[j], sn, ap[i].v[j]);
+        d.v[j] = lfma(k, lfma(sn, nmean, lmul(dx.v[j], w.v[j])), d.v[j]);
       }
-    }
-    float kh = 1.f;
-    if (p.w_post) {
-      float q[1] = {0.f};
+      if (p.dres && ok) store8(p.dres, row * p.D + c, f32<TP>(p, kR32), d);
+      if (gate) {
+        const F8 g = get(tg, kG32, i, at);
+        F8 dg;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        float h[8];
-        raw_get(rh[i], p.h32, h);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) q[0] = fmaf(h[j], h[j], q[0]);
-      }
-      row_sum(q, warps, red, buf);
-      kh = rsqrtf(fmaf(q[0], invD, p.eps));
-    }
-    float d[NV][8], wp[NV][8];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      raw_get(rs[i], p.ds32, d[i]);
-      const int c = 8 * (i * tpr + t);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) wp[i][j] = 1.f;
-      if (p.w_post && c < p.D) vec8(p.w_post, c, wp[i]);
-    }
-    // y_j of this thread (recomputed where it is needed: cheaper than keeping it)
-    auto y_of = [&](int i, int j, const float (&h)[8], const float (&g)[8]) {
-      float n = h[j] * kh * wp[i][j];
-      return p.g ? n * act(p.act, g[j]) : n;
-    };
-    if (p.w_pre) {
-      float q[2] = {0.f, 0.f};
-      float s[NV][8], dx[NV][8];
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = 8 * (i * tpr + t);
-        float h[8], g[8], r[8], sc[8], w[8];
-        raw_get(rh[i], p.h32, h);
-        raw_get(rg[i], p.g32, g);
-        raw_get(rr[i], p.r32, r);
-        raw_get(rx[i], p.dx32, dx[i]);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sc[j] = w[j] = 1.f;
-        if (c < p.D) {
-          if (p.scale) vec8(p.scale, c, sc);
-          vec8(p.w_pre, c, w);
+        for (int j = 0; j < 4; ++j) {
+          float2 a, da;
+          act.grad(g.v[j], a, da);
+          const float2 n = post ? lmul(hh[i].v[j], wp.v[j]) : hh[i].v[j], e = scale ? lmul(d.v[j], sc.v[j]) : d.v[j];
+          if (scale) as[i].v[j] = lfma(d.v[j], lmul(n, a), as[i].v[j]);
+          dg.v[j] = lmul(lmul(e, n), da);
+          d.v[j] = lmul(e, a);
         }
+        if (ok) store8(p.dg, row * p.D + c, f32<TP>(p, kG32), dg);
+      } else if (scale) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          s[i][j] = fmaf(sc[j], y_of(i, j, h, g), r[j]);
-          q[0] = fmaf(s[i][j], s[i][j], q[0]);
-          const float e = dx[i][j] * s[i][j];
-          q[1] = fmaf(e, w[j], q[1]);
+        for (int j = 0; j < 4; ++j) {
+          as[i].v[j] = lfma(d.v[j], post ? lmul(hh[i].v[j], wp.v[j]) : hh[i].v[j], as[i].v[j]);
+          d.v[j] = lmul(d.v[j], sc.v[j]);
         }
       }
-      row_sum(q, warps, red, buf);
-      const float k = rsqrtf(fmaf(q[0], invD, p.eps)), mean = q[1] * k * invD;
+      if (post)
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = 8 * (i * tpr + t);
-        if (c >= p.D) continue;
-        float w[8];
-        vec8(p.w_pre, c, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float sh = s[i][j] * k;
-          ap[i][j] = fmaf(dx[i][j], sh, ap[i][j]);
-          d[i][j] = fmaf(k, fmaf(dx[i][j], w[j], -sh * mean), d[i][j]);
+        for (int j = 0; j < 4; ++j) {
+          aw[i].v[j] = lfma(d.v[j], hh[i].v[j], aw[i].v[j]);
+          d.v[j] = lmul(kh, lfma(hh[i].v[j], nmean3, lmul(d.v[j], wp.v[j])));
         }
-      }
+      if (ok) store8(p.dh, row * p.D + c, f32<TP>(p, kH32), d);
     }
-    float q[1] = {0.f};
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = 8 * (i * tpr + t);
-      if (c >= p.D) continue;
-      if (p.dres) store8(p.dres, row * p.D + c, p.r32, d[i]);
-      float h[8], g[8], sc[8], dg[8];
-      raw_get(rh[i], p.h32, h);
-      raw_get(rg[i], p.g32, g);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) sc[j] = 1.f;
-      if (p.scale) vec8(p.scale, c, sc);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float hh = h[j] * kh, n = hh * wp[i][j];
-        float a = 1.f, da = 0.f;
-        if (p.g) act_grad(p.act, g[j], a, da);
-        as[i][j] = fmaf(d[i][j], n * a, as[i][j]);
-        const float e = d[i][j] * sc[j];
-        dg[j] = e * n * da;
-        d[i][j] = e * a;
-        if (p.w_post) {
-          aw[i][j] = fmaf(d[i][j], hh, aw[i][j]);
-          d[i][j] *= wp[i][j];
-          q[0] = fmaf(d[i][j], hh, q[0]);
-        }
-      }
-      if (p.g) store8(p.dg, row * p.D + c, p.g32, dg);
-    }
-    if (p.w_post) row_sum(q, warps, red, buf);
-    const float mean = q[0] * invD;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = 8 * (i * tpr + t);
-      if (c >= p.D) continue;
-      if (p.w_post) {
-        float h[8];
-        raw_get(rh[i], p.h32, h);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) d[i][j] = kh * fmaf(-h[j] * kh, mean, d[i][j]);
-      }
-      store8(p.dh, row * p.D + c, p.h32, d[i]);
-    }
+    at = next;
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
   if (!p.part) return;
+  float* const out = p.part + (size_t)blockIdx.x * 3 * p.D;
+  if (!kNarrow) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = 8 * (i * tpr + t);
-    if (c >= p.D) continue;
-    float* q = p.part + ((size_t)blockIdx.x * slots + slot) * 3 * p.D + c;
-    store8(q, 0, true, aw[i]);
-    store8(q + p.D, 0, true, as[i]);
-    store8(q + 2 * (size_t)p.D, 0, true, ap[i]);
+    for (int i = 0; i < NV; ++i) {
+      const int c = 8 * (i * tpr + t);
+      if (c >= p.D) continue;
+      store8(out + c, 0, true, aw[i]);
+      store8(out + p.D + c, 0, true, as[i]);
+      store8(out + 2 * (size_t)p.D + c, 0, true, ap[i]);
+    }
+    return;
+  }
+  // several rows a block: its slots' sums, in their order
+  float* const acc = reinterpret_cast<float*>(smem);  // [3][slots x 8 tpr]: 2048 channels each (256 threads of 8)
+  const int width = 8 * tpr;
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float* q = acc + slot * width + 8 * t + 2 * j;
+    q[0] = aw[0].v[j].x, q[1] = aw[0].v[j].y;
+    q[2048] = as[0].v[j].x, q[2049] = as[0].v[j].y;
+    q[4096] = ap[0].v[j].x, q[4097] = ap[0].v[j].y;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 3 * p.D; i += blockDim.x) {
+    const int k = i / p.D, c = i - k * p.D;
+    float v = 0.f;
+    for (int s = 0; s < slots; ++s) v += acc[k * 2048 + s * width + c];
+    out[i] = v;
   }
 }
 
@@ -347,6 +532,7 @@ __global__ void __launch_bounds__(256) norm_colsum(const float* __restrict__ par
   if (!out) return;  // the whole block
   float v = 0.f;
   if (c < D)
+#pragma unroll 4
     for (int i = y; i < P; i += 8) v += part[((size_t)i * 3 + blockIdx.y) * D + c];
   s[y][x] = v;
   __syncthreads();
@@ -359,19 +545,106 @@ __global__ void __launch_bounds__(256) norm_colsum(const float* __restrict__ par
 
 constexpr int kNormMaxD = 8192;
 
-// threads of a row, of a block and vectors of a thread for D channels
-void norm_shape(int D, int& nv, int& tpr, int& threads) {
-  nv = D <= 4096 ? 1 : 2;
-  tpr = 32 * ((D + 256 * nv - 1) / (256 * nv));
-  threads = tpr == 32 ? 256 : tpr;
+// Vectors of a thread, threads of a row and of a block for D channels.
+struct NormShape {
+  int nv, tpr, threads;
+  int slots() const { return threads / tpr; }
+};
+NormShape norm_shape(int D) {
+  NormShape s;
+  s.nv = D <= 4096 ? 1 : 2;
+  if (D <= 256) {
+    s.tpr = 1;
+    while (8 * s.tpr < D) s.tpr *= 2;
+    s.threads = 256;
+  } else {
+    s.tpr = s.threads = 32 * ((D + 256 * s.nv - 1) / (256 * s.nv));
+  }
+  return s;
 }
 
-int norm_bwd_blocks(long long N, int D) {
-  int nv, tpr, threads;
-  norm_shape(D, nv, tpr, threads);
-  const int slots = threads / tpr;
-  const long long most = 148 * std::max(1, 1024 / threads);
-  return (int)std::min<long long>((N + slots - 1) / slots, most);
+// Blocks: all that 148 SMs hold at once (`regs_threads` threads an SM by their
+// registers), or one for each of fewer groups of rows.
+int norm_blocks(long long N, const NormShape& s, int sm_threads) {
+  const long long most = 148 * std::max(1, sm_threads / s.threads);
+  return (int)std::min<long long>((N + s.slots() - 1) / s.slots(), most);
+}
+constexpr int kFwdThreads = 1024, kBwdThreads = 512;
+
+// The canonical type bits: those of absent tensors follow the others, so that
+// they do not take a call off its kernel.
+int canonical_types(const NormParams& p, bool s, bool x) {
+  int present = kH32 | (p.g ? kG32 : 0) | (p.res ? kR32 : 0) | (s ? kS32 : 0) | (x ? kX32 : 0);
+  int t = p.types & present;
+  if (t == present) return kH32 | kG32 | kR32 | kS32 | kX32;
+  if ((present & (kR32 | kS32)) == kR32 && (t & kR32)) t |= kS32;
+  if ((present & (kR32 | kS32)) == kS32 && (t & kS32)) t |= kR32;
+  return t;
+}
+
+template <int NV>
+void launch_fwd_t(const NormParams& p, int types, int blocks, const NormShape& s, cudaStream_t stream) {
+  switch (types) {
+    case 0: norm_fwd<NV, 0><<<blocks, s.threads, 0, stream>>>(p, s.tpr); break;
+    case kH32: norm_fwd<NV, kH32><<<blocks, s.threads, 0, stream>>>(p, s.tpr); break;
+    case kR32 | kS32: norm_fwd<NV, kR32 | kS32><<<blocks, s.threads, 0, stream>>>(p, s.tpr); break;
+    case kH32 | kR32 | kS32: norm_fwd<NV, kH32 | kR32 | kS32><<<blocks, s.threads, 0, stream>>>(p, s.tpr); break;
+    case 31: norm_fwd<NV, 31><<<blocks, s.threads, 0, stream>>>(p, s.tpr); break;
+    default: norm_fwd<NV, kAnyType><<<blocks, s.threads, 0, stream>>>(p, s.tpr); break;
+  }
+}
+// Rows of the adjoint's ring and its shared memory: up to four, as many as
+// leave room for the blocks that the registers allow on an SM (one for five
+// fp32 tensors of nearly 8192 channels).  The slots' sums of several rows a
+// block lie where the ring was.
+int bwd_ring(const NormParams& p, const NormShape& s, int& S) {
+  int es = 0;
+  for (auto [on, bit] : {std::pair<bool, int>{true, kH32}, {p.parts & kGate, kG32},
+                         {(p.parts & kRes) && (p.parts & kPre), kR32}, {p.parts & kDs, kS32}, {p.parts & kPre, kX32}})
+    if (on) es += p.types & bit ? 4 : 2;
+  const int row = s.threads * 8 * s.nv * es, room = 220 * 1024 / std::max(1, kBwdThreads / s.threads);
+  S = 4;
+  while (S > 1 && S * row > room) --S;
+  return std::max(S * row, s.slots() > 1 ? 3 * 2048 * 4 : 0);
+}
+
+template <int NV, bool kNarrow, int TP, int PT>
+int launch_bwd_k(const NormParams& p, int blocks, const NormShape& s, cudaStream_t stream) {
+  int S;
+  const int smem = bwd_ring(p, s, S);
+  cudaError_t e = cudaFuncSetAttribute(norm_bwd<NV, kNarrow, TP, PT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return (int)e;
+  norm_bwd<NV, kNarrow, TP, PT><<<blocks, s.threads, smem, stream>>>(p, s.tpr, S);
+  return (int)cudaGetLastError();
+}
+
+// The kernels that know types and parts: a norm before a block over a residual
+// stream; the gated norm after one; both in one, with and without a scale.
+constexpr int kPartsPre = kPre | kRes | kDs, kPartsPost = kPost | kGate | kDs,
+              kPartsBoth = kPost | kGate | kRes | kPre | kDs, kPartsAll = kPartsBoth | kScale;
+template <int TP>
+int launch_bwd_t(const NormParams& p, int blocks, const NormShape& s, cudaStream_t stream) {
+  switch (p.parts) {
+    case kPartsPre: return launch_bwd_k<1, false, TP, kPartsPre>(p, blocks, s, stream);
+    case kPartsPost: return launch_bwd_k<1, false, TP, kPartsPost>(p, blocks, s, stream);
+    case kPartsBoth: return launch_bwd_k<1, false, TP, kPartsBoth>(p, blocks, s, stream);
+    case kPartsAll: return launch_bwd_k<1, false, TP, kPartsAll>(p, blocks, s, stream);
+    default: return launch_bwd_k<1, false, TP, kAnyPart>(p, blocks, s, stream);
+  }
+}
+int launch_bwd(const NormParams& p, int blocks, const NormShape& s, cudaStream_t stream) {
+  if (s.nv == 2)
+    return p.types == kH32 && p.parts == kPartsAll ? launch_bwd_k<2, false, kH32, kPartsAll>(p, blocks, s, stream)
+                                                   : launch_bwd_k<2, false, kAnyType, kAnyPart>(p, blocks, s, stream);
+  if (s.slots() > 1) return launch_bwd_k<1, true, kAnyType, kAnyPart>(p, blocks, s, stream);
+  switch (p.types) {
+    case 0: return launch_bwd_t<0>(p, blocks, s, stream);
+    case kH32: return launch_bwd_t<kH32>(p, blocks, s, stream);
+    case kR32 | kS32: return launch_bwd_t<kR32 | kS32>(p, blocks, s, stream);
+    case kH32 | kR32 | kS32: return launch_bwd_t<kH32 | kR32 | kS32>(p, blocks, s, stream);
+    case 31: return launch_bwd_t<31>(p, blocks, s, stream);
+    default: return launch_bwd_k<1, false, kAnyType, kAnyPart>(p, blocks, s, stream);
+  }
 }
 
 }  // namespace
@@ -379,36 +652,29 @@ int norm_bwd_blocks(long long N, int D) {
 int norm_max_d() { return kNormMaxD; }
 
 size_t norm_part_floats(long long N, int D) {
-  int nv, tpr, threads;
-  norm_shape(D, nv, tpr, threads);
-  return (size_t)norm_bwd_blocks(N, D) * (threads / tpr) * 3 * D;
+  return (size_t)norm_blocks(N, norm_shape(D), kBwdThreads) * 3 * D;
 }
 
 int launch_norm_fwd(const NormParams& p, cudaStream_t stream) {
-  int nv, tpr, threads;
-  norm_shape(p.D, nv, tpr, threads);
-  const int slots = threads / tpr;
-  const unsigned grid = (unsigned)((p.N + slots - 1) / slots);
-  if (nv == 1)
-    norm_fwd<1><<<grid, threads, 0, stream>>>(p, tpr);
+  const NormShape s = norm_shape(p.D);
+  const int blocks = norm_blocks(p.N, s, kFwdThreads), types = canonical_types(p, p.s, p.x);
+  if (s.nv == 1)
+    launch_fwd_t<1>(p, types, blocks, s, stream);
   else
-    norm_fwd<2><<<grid, threads, 0, stream>>>(p, tpr);
+    launch_fwd_t<2>(p, types, blocks, s, stream);
   return (int)cudaGetLastError();
 }
 
 int launch_norm_bwd(NormParams p, float* dw_post, float* dscale, float* dw_pre, cudaStream_t stream) {
-  int nv, tpr, threads;
-  norm_shape(p.D, nv, tpr, threads);
+  const NormShape s = norm_shape(p.D);
+  const int blocks = norm_blocks(p.N, s, kBwdThreads);
+  p.types = canonical_types(p, p.ds, p.dx);
+  p.parts = (p.w_post ? kPost : 0) | (p.g ? kGate : 0) | (p.res ? kRes : 0) | (p.scale ? kScale : 0) |
+            (p.w_pre ? kPre : 0) | (p.ds ? kDs : 0);
   if (!dw_post && !dscale && !dw_pre) p.part = nullptr;
-  const int blocks = norm_bwd_blocks(p.N, p.D);
-  if (nv == 1)
-    norm_bwd<1><<<blocks, threads, 0, stream>>>(p, tpr);
-  else
-    norm_bwd<2><<<blocks, threads, 0, stream>>>(p, tpr);
-  int e = (int)cudaGetLastError();
+  const int e = launch_bwd(p, blocks, s, stream);
   if (e || !p.part) return e;
-  norm_colsum<<<dim3((p.D + 31) / 32, 3), 256, 0, stream>>>(p.part, blocks * (threads / tpr), p.D, dw_post,
-                                                            dscale, dw_pre);
+  norm_colsum<<<dim3((p.D + 31) / 32, 3), 256, 0, stream>>>(p.part, blocks, p.D, dw_post, dscale, dw_pre);
   return (int)cudaGetLastError();
 }
 

@@ -9,11 +9,11 @@ namespace pararnn {
 struct NormParams {
   const void *h, *g, *res, *ds, *dx;
   long long ld_h, ld_g, ld_r, ld_ds, ld_dx;  // row strides in elements
-  bool h32, g32, r32, ds32, dx32;            // fp32 (else bf16)
+  int types;                                 // bits 0-4: h, g, res, s (ds), x (dx) are fp32, else bf16
+  int parts;                                 // adjoint: bits of the parts present (set at the launch)
   const float *w_post, *scale, *w_pre;
   int act;
   void *s, *x;                               // forward outputs [N][D]
-  bool s32, x32;
   void *dh, *dg, *dres;                      // adjoint outputs [N][D], types of h, g, res
   float* part;                               // adjoint: [blocks][3][D] sums
   float eps;

@@ -31,6 +31,9 @@ __device__ __forceinline__ float2 ex2_2(float2 v) { return make_float2(ex2(v.x),
 __device__ __forceinline__ float2 ex2_neg_abs(float2 v) { return make_float2(ex2(-fabsf(v.x)), ex2(-fabsf(v.y))); }
 __device__ __forceinline__ float2 rcp_2(float2 v) { return make_float2(rcp(v.x), rcp(v.y)); }
 __device__ __forceinline__ float2 neg2(float2 v) { return make_float2(-v.x, -v.y); }
+// 2^v that overflowed made finite again, so that it times its 1 / (1 + 2^v) = 0
+// is not NaN
+__device__ __forceinline__ float2 finite(float2 t) { return make_float2(fminf(t.x, 8.5e37f), fminf(t.y, 8.5e37f)); }
 // v > 0 ? a : b
 __device__ __forceinline__ float2 sel_pos(float2 v, float2 a, float2 b) {
   return make_float2(v.x > 0.f ? a.x : b.x, v.y > 0.f ? a.y : b.y);
@@ -111,9 +114,9 @@ struct LinCell<PARARNN_LIN_GRU> {
   // keeps of it: z (1 - z), of its own size where z is near 1 too.
   static constexpr int kKeep = 1;
   __device__ __forceinline__ void head(float2 u0, float2& nm, float2 (&keep)[kKeep]) const {
-    const float2 v = zarg(u0), t = ex2_neg_abs(v), q = rcp_2(ladd(t, both(1.f))), tq = lmul(t, q);
-    keep[0] = lmul(tq, q);
-    nm = make_float2(v.x > 0.f ? -tq.x : -q.x, v.y > 0.f ? -tq.y : -q.y);
+    const float2 t = ex2_2(zarg(u0));
+    nm = rcp_2(neg2(ladd(t, both(1.f))));
+    keep[0] = lmul(lmul(finite(t), nm), nm);
   }
   // The second: du of one step from lambda and h_{t-1}.
   __device__ __forceinline__ void grad(const float2 (&u)[G], float2 nm, const float2 (&keep)[kKeep], float2 hp,
@@ -137,7 +140,8 @@ struct LinCell<PARARNN_LIN_DECAY> {
     k = lmul(make_float2(softplus(lam[d]), softplus(lam[d + 1])), both(kappa * kLog2e));
   }
   __device__ __forceinline__ void coef(const float2 (&u)[G], float2& nm, float2& b) const {
-    // r and i over one reciprocal: sig(x) is q = 1 / (1 + 2^-|v|) for x >= 0
+    // r and i over one reciprocal (this cell's solve is bound by the
+    // special-function unit): sig(x) is q = 1 / (1 + 2^-|v|) for x >= 0
     // (v <= 0), 2^-|v| q below
     const float2 vr = lfma(u[0], both(-kLog2e), br), vi = lfma(u[1], both(-kLog2e), bi);
     const float2 tr = ex2_neg_abs(vr), ti = ex2_neg_abs(vi);
@@ -151,16 +155,14 @@ struct LinCell<PARARNN_LIN_DECAY> {
   // kept for the second pass: w = -log a and 1 - r
   static constexpr int kKeep = 2;
   __device__ __forceinline__ void head(float2 u0, float2& nm, float2 (&keep)[kKeep]) const {
-    const float2 v = lfma(u0, both(-kLog2e), br), t = ex2_neg_abs(v), q = rcp_2(ladd(t, both(1.f)));
-    const float2 tq = lmul(t, q), w = lmul(k, sel_pos(v, tq, q));
+    const float2 t = ex2_2(lfma(u0, both(-kLog2e), br)), r = rcp_2(ladd(t, both(1.f))), w = lmul(k, r);
     nm = decay_nm(w);
     keep[0] = lmul(w, both(kLn2));
-    keep[1] = sel_pos(v, q, tq);
+    keep[1] = lmul(finite(t), r);  // where r is 0, so is all that it multiplies
   }
   __device__ __forceinline__ void grad(const float2 (&u)[G], float2 nm, const float2 (&keep)[kKeep], float2 hp,
                                        float2 lt, float2 (&du)[G], float2& e) const {
-    const float2 v = lfma(u[1], both(-kLog2e), bi), t = ex2_neg_abs(v), q = rcp_2(ladd(t, both(1.f)));
-    const float2 tq = lmul(t, q), i = sel_pos(v, tq, q);
+    const float2 t = ex2_2(lfma(u[1], both(-kLog2e), bi)), i = rcp_2(ladd(t, both(1.f)));
     const float2 x = ladd(u[2], bx), a = ladd(nm, both(1.f)), w = keep[0];
     const float2 s = lmul(neg2(nm), ladd(nm, both(2.f)));  // beta^2
     // 1 / beta; w / beta -> 0 with w
@@ -171,7 +173,7 @@ struct LinCell<PARARNN_LIN_DECAY> {
     e = lmul(lw, lfma(lmul(a, rb), lmul(i, x), neg2(hp)));
     du[0] = lmul(e, keep[1]);
     const float2 lb = lmul(lt, lmul(s, rb));
-    du[1] = lmul(lmul(lb, x), lmul(tq, q));
+    du[1] = lmul(lmul(lb, x), lmul(lmul(finite(t), i), i));
     du[2] = lmul(lb, i);
   }
   static __device__ __forceinline__ float2 lam_scale(const float* lam, int d) {

@@ -77,6 +77,11 @@ def test_widths_match_the_oracle(cuda_ok, D):
     check(*draw(7, D, **FULL, wide=True, seed=D))
 
 
+@pytest.mark.parametrize("D", [4096, 8192])
+def test_widths_of_all_fp32_rows(cuda_ok, D):
+    check(*draw(300, D, **KINDS["full_f32"], seed=D))
+
+
 @pytest.mark.parametrize("N", [1, 2, 8, 9, 147, 1000, 5000])
 def test_row_counts_match_the_oracle(cuda_ok, N):
     check(*draw(N, 72, **FULL, seed=N))

@@ -269,10 +269,17 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
-// One tensor of the adjoint's ring: this thread's channels of the next row to
-// copy, the bytes from a row to the thread's next, and where they lie in a
-// slot (16-byte pieces, the threads' side by side; `second`: from the first
-// piece of 8 fp32 channels to the other).
+// `bytes` (a multiple of 16) into shared memory, counted by `bar`
+__device__ __forceinline__ void copy_bulk(uint32_t dst, const void* src, unsigned bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+constexpr uint64_t kNormWaitNs = 2000000000ull;
+
+// One tensor of the adjoint's ring: the next row to copy (of a narrow row, this
+// thread's channels of it), the bytes to the one after, and where it lies in a
+// slot.
 struct RingTensor {
   const char* at;
   long long step;
@@ -288,39 +295,37 @@ struct RingTensor {
 // norm's sums give, so one exchange serves a row: sums of s^2, s e, ds z, e z
 // and s z (e = dx w_pre), and of the next row's h^2.
 //
-// Every thread copies its own channels of its rows to come into a ring of `S`
-// rows in shared memory (cp.async) and reads them from there where it needs
-// them: five tensors of a row and a row ahead do not fit beside the weights and
-// their sums in the registers.  The sums leave once per block.
+// Rows to come wait in a ring of `S` rows in shared memory, from where threads
+// read what they need: five tensors of a row and a row ahead do not fit beside
+// the weights and their sums in the registers.  A row that is the block's comes
+// by one bulk copy a tensor, which thread 0 issues after the exchange that ends
+// the last use of its slot; of narrow rows (kNarrow: of a warp at most, several
+// a block) every thread copies its own channels.  The sums leave once per block.
 template <int NV, bool kNarrow, int TP, int PT>
 __global__ void __launch_bounds__(512) norm_bwd(const NormParams p, const int tpr, const int S) {
   extern __shared__ __align__(16) char smem[];
   __shared__ __align__(16) NormShared6 sh;
-  // kNarrow: rows of a warp at most, several a block; else a row is the block's
+  __shared__ uint64_t full[4];
   const int threads = blockDim.x, slots = kNarrow ? threads / tpr : 1, slot = kNarrow ? threadIdx.x / tpr : 0;
   const int t = kNarrow ? threadIdx.x % tpr : threadIdx.x;
-  const int piece = 16 * threads;
   const long long step = (long long)gridDim.x * slots;
   const float invD = 1.f / (float)p.D;
   const Act act = {p.act == PARARNN_ACT_SILU};
   int buf = 0;
   long long row = (long long)blockIdx.x * slots + slot;
+  const bool post = has<PT>(p, kPost), gate = has<PT>(p, kGate), pre = has<PT>(p, kPre), res = has<PT>(p, kRes),
+             sum = res && pre, scale = has<PT>(p, kScale), dsum = has<PT>(p, kDs);
   int bytes = 0;  // of a slot of the ring
-  const bool post = has<PT>(p, kPost), gate = has<PT>(p, kGate), pre = has<PT>(p, kPre),
-             res = has<PT>(p, kRes), sum = has<PT>(p, kRes) && pre, scale = has<PT>(p, kScale), dsum = has<PT>(p, kDs);
   auto tensor = [&](const void* q, long long ld, int bit, bool on) {
     const int es = f32<TP>(p, bit) ? 4 : 2;
-    RingTensor r = {static_cast<const char*>(q) + (row * ld + 8 * t) * es, step * ld * es, bytes};
-    if (on) bytes += NV * (es / 2) * piece;
+    RingTensor r = {static_cast<const char*>(q) + (row * ld + (kNarrow ? 8 * t : 0)) * es, step * ld * es, bytes};
+    if (on) bytes += (kNarrow ? 8 * threads : p.D) * es;
     return r;
   };
   RingTensor th = tensor(p.h, p.ld_h, kH32, true), tg = tensor(p.g, p.ld_g, kG32, gate),
              tr = tensor(p.res, p.ld_r, kR32, sum), ts = tensor(p.ds, p.ld_ds, kS32, dsum),
              tx = tensor(p.dx, p.ld_dx, kX32, pre);
-  // a thread with channels past D starts from zeros and never copies those
-  if (8 * ((NV - 1) * tpr + t) >= p.D)
-    for (int i = threadIdx.x * 16; i < S * bytes; i += piece)
-      *reinterpret_cast<uint4*>(smem + i) = make_uint4(0, 0, 0, 0);
+  if (!kNarrow && threadIdx.x < 4) mbar_init(&full[threadIdx.x], 1);
   if (threadIdx.x < kNormWarps)
     for (int i = 0; i < 12; ++i) (&sh.red[0][0][0])[i * kNormWarps + threadIdx.x] = 0.f;
   __syncthreads();
@@ -336,49 +341,58 @@ __global__ void __launch_bounds__(512) norm_bwd(const NormParams p, const int tp
     return weights(k == 0 ? p.w_post : k == 1 ? p.scale : p.w_pre, c, c < p.D);
   };
   const uint32_t base = smem_u32(smem);
-  // past N nothing is copied; where a block has several rows, the last ones of
-  // its last round become zeros
-  auto copy1 = [&](RingTensor& r, int bit, bool in, int k) {
-    const bool wide = f32<TP>(p, bit);
+  auto copy1 = [&](RingTensor& r, int bit, bool on, bool in, int k) {
+    if (!on) return;
+    const int es = f32<TP>(p, bit) ? 4 : 2;
+    if (!kNarrow) {
+      if (in) copy_bulk(base + k * bytes + r.offset, r.at, p.D * es, &full[k]);
+    } else {
+      const int to = k * bytes + r.offset + 8 * threadIdx.x * es;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if (8 * (i * tpr + t) >= p.D) continue;
-      const char* q = r.at + i * (8 * tpr * (wide ? 4 : 2));
-      const int to = 16 * threadIdx.x + k * bytes + r.offset + i * piece;
-      if (in) {
-        copy16(base + to, q);
-        if (wide) copy16(base + to + NV * piece, q + 16);
-      } else if (kNarrow) {
-        *reinterpret_cast<uint4*>(smem + to) = make_uint4(0, 0, 0, 0);
-        if (wide) *reinterpret_cast<uint4*>(smem + to + NV * piece) = make_uint4(0, 0, 0, 0);
-      }
+      for (int i = 0; i < 2; ++i)
+        if (i == 0 || es == 4) {
+          // past D and N there are zeros
+          if (in && 8 * t < p.D)
+            copy16(base + to + 16 * i, r.at + 16 * i);
+          else
+            *reinterpret_cast<uint4*>(smem + to + 16 * i) = make_uint4(0, 0, 0, 0);
+        }
     }
     r.at += r.step;
   };
   auto copy = [&](long long row, int k) {  // the next row, into slot k
-    copy1(th, kH32, row < p.N, k);
-    if (gate) copy1(tg, kG32, row < p.N, k);
-    if (sum) copy1(tr, kR32, row < p.N, k);
-    if (dsum) copy1(ts, kS32, row < p.N, k);
-    if (pre) copy1(tx, kX32, row < p.N, k);
-    asm volatile("cp.async.commit_group;" ::: "memory");
+    const bool in = row < p.N;
+    if (!kNarrow && in) mbar_arrive_expect_tx(&full[k], bytes);
+    copy1(th, kH32, true, in, k);
+    copy1(tg, kG32, gate, in, k);
+    copy1(tr, kR32, sum, in, k);
+    copy1(ts, kS32, dsum, in, k);
+    copy1(tx, kX32, pre, in, k);
+    if (kNarrow) asm volatile("cp.async.commit_group;" ::: "memory");
   };
   auto get = [&](const RingTensor& r, int bit, int i, int k, bool on = true) {
-    if (!on) return F8{both(0.f), both(0.f), both(0.f), both(0.f)};
-    const char* q = smem + 16 * threadIdx.x + k * bytes + r.offset + i * piece;
-    Raw8 v;
-    v.a = *reinterpret_cast<const uint4*>(q);
-    v.b = f32<TP>(p, bit) ? *reinterpret_cast<const uint4*>(q + NV * piece) : v.a;
-    return raw_get(v, f32<TP>(p, bit));
+    const int c = 8 * (i * tpr + t), es = f32<TP>(p, bit) ? 4 : 2;
+    Raw8 v = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    if (on && (kNarrow || c < p.D)) {
+      const uint4* q = reinterpret_cast<const uint4*>(smem + k * bytes + r.offset + (kNarrow ? 8 * threadIdx.x : c) * es);
+      v.a = q[0];
+      if (es == 4) v.b = q[1];
+    }
+    return raw_get(v, es == 4);
   };
-  // all but the `S - 2` latest copies are there: this row's and the next one's
-  auto wait = [&]() {
-    if (S == 4)
+  // Until row r is in slot k; of narrow rows, all but the S - 2 latest copies.
+  // A wait that runs out makes the rest of the block's rows NaN.
+  bool lost = false;
+  auto wait = [&](unsigned r, int k) {
+    if (!kNarrow) {
+      if (!lost) lost = !mbar_wait_bounded(&full[k], (r / S) & 1, kNormWaitNs);
+    } else if (S == 4) {
       asm volatile("cp.async.wait_group 2;" ::: "memory");
-    else if (S == 3)
+    } else if (S == 3) {
       asm volatile("cp.async.wait_group 1;" ::: "memory");
-    else
+    } else {
       asm volatile("cp.async.wait_group 0;" ::: "memory");
+    }
   };
   auto squares = [&](int k) {
     float q = 0.f;
@@ -394,21 +408,32 @@ __global__ void __launch_bounds__(512) norm_bwd(const NormParams p, const int tp
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) aw[i].v[j] = as[i].v[j] = ap[i].v[j] = both(0.f);
-  for (int k = 0; k < S - 1; ++k) copy(row + k * step, k);
+  // the rows of the ring, but one slot for which the first exchange must pass
+  if (kNarrow || threadIdx.x == 0)
+    for (int k = 0; k < S - 1; ++k) copy(row + k * step, k);
   float kh1 = 1.f;  // 1 / rms(h) of the row at hand
-  auto first_norm = [&]() {
-    wait();
+  auto first_norm = [&](unsigned r) {
+    wait(r, 0);
     float q[6] = {squares(0), 0.f, 0.f, 0.f, 0.f, 0.f};
     row_sum6<kNarrow>(q, tpr, sh, buf);
     kh1 = rsqrtf(fmaf(q[0], invD, p.eps));
   };
-  if (post && S > 1) first_norm();
+  if (post && S > 1) first_norm(0);
   int at = 0;  // slot of the row at hand
-  for (long long r0 = (long long)blockIdx.x * slots; r0 < p.N; r0 += step, row += step) {
-    copy(row + (S - 1) * step, at == 0 ? S - 1 : at - 1);
+  unsigned nr = 0;
+  for (long long r0 = (long long)blockIdx.x * slots; r0 < p.N; r0 += step, row += step, ++nr) {
     const int next = at + 1 == S ? 0 : at + 1;
-    if (S == 1 && post) first_norm();  // a ring of one row: nothing is ahead
-    wait();
+    if (kNarrow) {
+      copy(row + (S - 1) * step, at == 0 ? S - 1 : at - 1);
+    } else if (S == 1) {  // a ring of one row: nothing is ahead
+      __syncthreads();
+      if (threadIdx.x == 0) copy(row, 0);
+    }
+    if (S == 1 && post) first_norm(nr);
+    wait(nr, at);
+    const bool ahead = post && S > 1 && row + step < p.N;
+    if (!kNarrow && ahead) wait(nr + 1, next);
+    if (lost) kh1 = __int_as_float(0x7fffffff);
     const float2 kh = both(kh1);
     float q[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     F8 hh[NV], s[NV];
@@ -438,8 +463,10 @@ __global__ void __launch_bounds__(512) norm_bwd(const NormParams p, const int tp
         q[4] = dot8(s[i], z, q[4]);
       }
     }
-    if (post) q[5] = squares(next);
+    if (ahead || (kNarrow && post)) q[5] = squares(next);
     row_sum6<kNarrow>(q, tpr, sh, buf);
+    // every thread is done with the row before: its slot takes a row again
+    if (!kNarrow && S > 1 && threadIdx.x == 0) copy(row + (S - 1) * step, at == 0 ? S - 1 : at - 1);
     const float k1 = pre ? rsqrtf(fmaf(q[0], invD, p.eps)) : 0.f, nm1 = -(q[1] * k1 * invD);
     const float2 k = both(k1), nmean = both(nm1);
     const float2 nmean3 = both(-(fmaf(k1, fmaf(k1 * nm1, q[4], q[3]), q[2]) * invD));
@@ -489,7 +516,7 @@ __global__ void __launch_bounds__(512) norm_bwd(const NormParams p, const int tp
     }
     at = next;
   }
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  if (kNarrow) asm volatile("cp.async.wait_group 0;" ::: "memory");
   if (!p.part) return;
   float* const out = p.part + (size_t)blockIdx.x * 3 * p.D;
   if (!kNarrow) {
@@ -602,7 +629,7 @@ int bwd_ring(const NormParams& p, const NormShape& s, int& S) {
   for (auto [on, bit] : {std::pair<bool, int>{true, kH32}, {p.parts & kGate, kG32},
                          {(p.parts & kRes) && (p.parts & kPre), kR32}, {p.parts & kDs, kS32}, {p.parts & kPre, kX32}})
     if (on) es += p.types & bit ? 4 : 2;
-  const int row = s.threads * 8 * s.nv * es, room = 220 * 1024 / std::max(1, kBwdThreads / s.threads);
+  const int row = (s.slots() > 1 ? 8 * s.threads : p.D) * es, room = 220 * 1024 / std::max(1, kBwdThreads / s.threads);
   S = 4;
   while (S > 1 && S * row > room) --S;
   return std::max(S * row, s.slots() > 1 ? 3 * 2048 * 4 : 0);

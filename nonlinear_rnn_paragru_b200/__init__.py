@@ -503,10 +503,17 @@ def seq_baseline(cell, u, a, bias=None, c0=None, h0=None, stream=None):
 # one is, and allocate what they return (and their scratch) on the stream they
 # launch on, so both live as long as the work in flight, in a captured graph
 # too.  Inputs made on another stream are the caller's to order, as with every
-# CUDA call.
-_DTYPES = {torch.float32: PARARNN_F32, torch.bfloat16: PARARNN_BF16}
+# CUDA call.  A decode step takes the GPU 2 us, so the checks are written to
+# cost little.
+_F32, _BF16 = torch.float32, torch.bfloat16
+_DTYPES = {_F32: PARARNN_F32, _BF16: PARARNN_BF16}
+_FLOATS = (_F32, _BF16)
+_MASKS = (torch.bool, torch.uint8)
 _LIN_CELLS = {PARARNN_LIN_GRU: 2, PARARNN_LIN_DECAY: 3}
 _ACTS = {"silu": PARARNN_ACT_SILU, "sigmoid": PARARNN_ACT_SIGMOID}
+# the current stream's handle, without building a Stream object
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _code(t):
@@ -514,7 +521,7 @@ def _code(t):
     return 0 if t is None else _DTYPES.get(t.dtype, -1)
 
 
-def _need(t, name, shape, device, dtypes=(torch.float32,)):
+def _need(t, name, shape, device, dtypes=(_F32,)):
     """Pointer of a contiguous tensor of this shape, one of these types, on
     this device (None -> NULL)."""
     if t is None:
@@ -562,23 +569,28 @@ def _lin_u(cell, u, ndim):
     if G is None:
         raise PararnnError(-1, f"linear recurrence: unknown cell {cell}")
     dev = _first(u, "u")
-    if u.dim() != ndim or u.shape[-2] != G:
+    shape = u.shape
+    if len(shape) != ndim or shape[-2] != G:
         raise ValueError(f"u: expected {'[B, T, G, D]' if ndim == 4 else '[B, G, D]'} with G = {G},"
-                         f" got {tuple(u.shape)}")
-    if u.stride(-1) != 1 and u.shape[-1] > 1:
+                         f" got {tuple(shape)}")
+    st = u.stride()
+    if st[-1] != 1 and shape[-1] > 1:
         raise ValueError("u: channels must be contiguous")
-    return dev, G
+    # an axis of one has no stride
+    return dev, G, [0 if n == 1 else k for n, k in zip(shape[:-1], st)]
 
 
-def _lin_strides(u):
-    """(batch, [step,] gate) strides in elements; an axis of one has none."""
-    return [0 if n == 1 else s for n, s in zip(u.shape[:-1], u.stride()[:-1])]
+def _lin_params(cell, dev, B, G, D, lam, bias, h0, h0_name="h0"):
+    if (lam is None) != (cell == PARARNN_LIN_GRU):
+        raise ValueError("lam: given exactly for PARARNN_LIN_DECAY")
+    return (_need(lam, "lam", (D,), dev), _need(bias, "bias", (G, D), dev),
+            _need(h0, h0_name, (B, D), dev))
 
 
 def pararnn_linrec_solve(cell, u, lam, bias, h0, reset, h, kappa=8.0, stream=None):
     B, T, G, D = u.shape
     _check(load_library().pararnn_linrec_solve(
-        cell, u.data_ptr(), _code(u), *_lin_strides(u), _ptr(lam), _ptr(bias), _ptr(h0),
+        cell, u.data_ptr(), _code(u), *_lin_u(cell, u, 4)[2], _ptr(lam), _ptr(bias), _ptr(h0),
         _ptr(reset, None), _ptr(h), B, T, D, kappa, _stream(stream)), "pararnn_linrec_solve")
 
 
@@ -590,7 +602,7 @@ def pararnn_linrec_adjoint(cell, u, lam, bias, h0, reset, h, dLdh, du, dlam, dbi
                            workspace, kappa=8.0, stream=None):
     B, T, G, D = u.shape
     _check(load_library().pararnn_linrec_adjoint(
-        cell, u.data_ptr(), _code(u), *_lin_strides(u), _ptr(lam), _ptr(bias), _ptr(h0),
+        cell, u.data_ptr(), _code(u), *_lin_u(cell, u, 4)[2], _ptr(lam), _ptr(bias), _ptr(h0),
         _ptr(reset, None), _ptr(h), _ptr(dLdh), _ptr(du, None), _code(du), _ptr(dlam),
         _ptr(dbias), _ptr(dh0), B, T, D, kappa, _wptr(workspace),
         workspace.numel() * workspace.element_size(), _stream(stream)),
@@ -600,19 +612,8 @@ def pararnn_linrec_adjoint(cell, u, lam, bias, h0, reset, h, dLdh, du, dlam, dbi
 def pararnn_linrec_step(cell, u_t, lam, bias, h_prev, h_next, kappa=8.0, stream=None):
     B, G, D = u_t.shape
     _check(load_library().pararnn_linrec_step(
-        cell, u_t.data_ptr(), _code(u_t), *_lin_strides(u_t), _ptr(lam), _ptr(bias),
+        cell, u_t.data_ptr(), _code(u_t), *_lin_u(cell, u_t, 3)[2], _ptr(lam), _ptr(bias),
         _ptr(h_prev), _ptr(h_next), B, D, kappa, _stream(stream)), "pararnn_linrec_step")
-
-
-_MASKS = (torch.bool, torch.uint8)
-
-
-def _lin_params(cell, dev, B, G, D, lam, bias, h0, h0_name="h0"):
-    if (lam is None) != (cell == PARARNN_LIN_GRU):
-        raise ValueError("lam: given exactly for PARARNN_LIN_DECAY")
-    _need(lam, "lam", (D,), dev)
-    _need(bias, "bias", (G, D), dev)
-    _need(h0, h0_name, (B, D), dev)
 
 
 def linrec_solve(cell, u, lam=None, bias=None, h0=None, *, reset=None, kappa=8.0, out=None,
@@ -623,15 +624,19 @@ def linrec_solve(cell, u, lam=None, bias=None, h0=None, *, reset=None, kappa=8.0
     (channels contiguous, strides multiples of 8 elements, 16-byte aligned).
     reset [B, T] (bool or uint8): the state that enters a marked step is zero.
     `out`: the tensor to write h to."""
-    dev, G = _lin_u(cell, u, 4)
+    dev, G, st = _lin_u(cell, u, 4)
     B, T, _, D = u.shape
-    _lin_params(cell, dev, B, G, D, lam, bias, h0)
-    _need(reset, "reset", (B, T), dev, _MASKS)
-    _need(out, "out", (B, T, D), dev)
+    lp, bp, hp = _lin_params(cell, dev, B, G, D, lam, bias, h0)
+    rp = _need(reset, "reset", (B, T), dev, _MASKS)
+    op = _need(out, "out", (B, T, D), dev)
     with _on(dev, stream):
-        h = torch.empty((B, T, D), dtype=torch.float32, device=dev) if out is None else out
-        pararnn_linrec_solve(cell, u, lam, bias, h0, reset, h, kappa)
-    return h
+        if out is None:
+            out = u.new_empty((B, T, D), dtype=_F32)
+            op = out.data_ptr()
+        _check(load_library().pararnn_linrec_solve(
+            cell, u.data_ptr(), _code(u), *st, lp, bp, hp, rp, op, B, T, D, kappa,
+            _raw_stream(dev.index)), "pararnn_linrec_solve")
+    return out
 
 
 def linrec_adjoint(cell, u, lam, bias, h0, h, dLdh, *, reset=None, kappa=8.0, want_params=True,
@@ -640,55 +645,61 @@ def linrec_adjoint(cell, u, lam, bias, h0, h, dLdh, *, reset=None, kappa=8.0, wa
     [B, T, G, D] (u's type, or `du_dtype` = torch.float32), dlam [D], dbias
     [G, D] and dh0 [B, D] (None where not wanted or absent).  `out`: a dict of
     tensors to write to instead of new ones."""
-    dev, G = _lin_u(cell, u, 4)
+    dev, G, st = _lin_u(cell, u, 4)
     B, T, _, D = u.shape
-    _lin_params(cell, dev, B, G, D, lam, bias, h0)
-    _need(reset, "reset", (B, T), dev, _MASKS)
+    lp, bp, hp = _lin_params(cell, dev, B, G, D, lam, bias, h0)
+    rp = _need(reset, "reset", (B, T), dev, _MASKS)
     if h is None or dLdh is None:
         raise ValueError("h and dLdh are needed")
-    _need(h, "h", (B, T, D), dev)
-    _need(dLdh, "dLdh", (B, T, D), dev)
+    sp, gp = _need(h, "h", (B, T, D), dev), _need(dLdh, "dLdh", (B, T, D), dev)
     o = out or {}
-    _need(o.get("du"), "du", u.shape, dev, (torch.float32, torch.bfloat16))
     with _on(dev, stream):
-        def new(name, shape, dtype=torch.float32):
+        def new(name, shape, dtype=_F32, dtypes=(_F32,)):
             t = o.get(name)
             if t is None:
-                return torch.empty(shape, dtype=dtype, device=dev)
-            if name != "du":
-                _need(t, name, shape, dev)
-            return t
-        du = new("du", (B, T, G, D), du_dtype or u.dtype)
-        dlam = new("dlam", (D,)) if want_params and cell == PARARNN_LIN_DECAY else None
-        dbias = new("dbias", (G, D)) if want_params else None
-        dh0 = new("dh0", (B, D)) if want_dh0 else None
-        ws = torch.empty(max(256, pararnn_linrec_workspace_size(cell, B, T, D)), dtype=torch.uint8,
-                         device=dev)
-        pararnn_linrec_adjoint(cell, u, lam, bias, h0, reset, h, dLdh, du, dlam, dbias, dh0, ws,
-                               kappa)
+                t = u.new_empty(shape, dtype=dtype)
+                return t, t.data_ptr()
+            return t, _need(t, name, shape, dev, dtypes)
+        du, dup = new("du", (B, T, G, D), du_dtype or u.dtype, _FLOATS)
+        dlam, dlp = new("dlam", (D,)) if want_params and lam is not None else (None, None)
+        dbias, dbp = new("dbias", (G, D)) if want_params else (None, None)
+        dh0, dhp = new("dh0", (B, D)) if want_dh0 else (None, None)
+        lib = load_library()
+        nbytes = max(256, lib.pararnn_linrec_workspace_size(cell, B, T, D))
+        ws = u.new_empty(nbytes, dtype=torch.uint8)
+        _check(lib.pararnn_linrec_adjoint(
+            cell, u.data_ptr(), _code(u), *st, lp, bp, hp, rp, sp, gp, dup, _code(du), dlp, dbp, dhp,
+            B, T, D, kappa, ws.data_ptr(), nbytes, _raw_stream(dev.index)), "pararnn_linrec_adjoint")
     return {"du": du, "dlam": dlam, "dbias": dbias, "dh0": dh0}
 
 
 def linrec_step(cell, u_t, lam=None, bias=None, h_prev=None, *, kappa=8.0, out=None, stream=None):
     """One decode step of the gated linear recurrence: u_t [B, G, D] -> the
     next state [B, D].  `out` may be `h_prev` (in-place update)."""
-    dev, G = _lin_u(cell, u_t, 3)
+    dev, G, st = _lin_u(cell, u_t, 3)
     B, _, D = u_t.shape
-    _lin_params(cell, dev, B, G, D, lam, bias, h_prev, "h_prev")
-    _need(out, "out", (B, D), dev)
+    lp, bp, hp = _lin_params(cell, dev, B, G, D, lam, bias, h_prev, "h_prev")
+    op = _need(out, "out", (B, D), dev)
     with _on(dev, stream):
-        h = torch.empty((B, D), dtype=torch.float32, device=dev) if out is None else out
-        pararnn_linrec_step(cell, u_t, lam, bias, h_prev, h, kappa)
-    return h
+        if out is None:
+            out = u_t.new_empty((B, D), dtype=_F32) if h_prev is None else torch.empty_like(h_prev)
+            op = out.data_ptr()
+        _check(load_library().pararnn_linrec_step(
+            cell, u_t.data_ptr(), _code(u_t), *st, lp, bp, hp, op, B, D, kappa,
+            _raw_stream(dev.index)), "pararnn_linrec_step")
+    return out
+
+
+def _any_ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def pararnn_block_norm(h, h_stride, gate, gate_stride, act, w_post, res, res_stride, scale, w_pre, s,
                        x, eps, N, D, stream=None):
     _check(load_library().pararnn_block_norm(
-        h.data_ptr(), _code(h), h_stride, None if gate is None else gate.data_ptr(), _code(gate),
-        gate_stride, act, _ptr(w_post), None if res is None else res.data_ptr(), _code(res),
-        res_stride, _ptr(scale), _ptr(w_pre), _ptr(s, None), _code(s), _ptr(x, None), _code(x), eps,
-        N, D, _stream(stream)), "pararnn_block_norm")
+        h.data_ptr(), _code(h), h_stride, _any_ptr(gate), _code(gate), gate_stride, act, _ptr(w_post),
+        _any_ptr(res), _code(res), res_stride, _ptr(scale), _ptr(w_pre), _ptr(s, None), _code(s),
+        _ptr(x, None), _code(x), eps, N, D, _stream(stream)), "pararnn_block_norm")
 
 
 def pararnn_block_norm_workspace_size(N, D) -> int:
@@ -699,22 +710,23 @@ def pararnn_block_norm_adjoint(h, h_stride, gate, gate_stride, act, w_post, res,
                                w_pre, ds, ds_stride, dx, dx_stride, dh, dgate, dres, dw_post, dscale,
                                dw_pre, eps, N, D, workspace, stream=None):
     _check(load_library().pararnn_block_norm_adjoint(
-        h.data_ptr(), _code(h), h_stride, None if gate is None else gate.data_ptr(), _code(gate),
-        gate_stride, act, _ptr(w_post), None if res is None else res.data_ptr(), _code(res),
-        res_stride, _ptr(scale), _ptr(w_pre), None if ds is None else ds.data_ptr(), _code(ds),
-        ds_stride, None if dx is None else dx.data_ptr(), _code(dx), dx_stride, _ptr(dh, None),
-        _ptr(dgate, None), _ptr(dres, None), _ptr(dw_post), _ptr(dscale), _ptr(dw_pre), eps, N, D,
-        _wptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)),
+        h.data_ptr(), _code(h), h_stride, _any_ptr(gate), _code(gate), gate_stride, act, _ptr(w_post),
+        _any_ptr(res), _code(res), res_stride, _ptr(scale), _ptr(w_pre), _any_ptr(ds), _code(ds),
+        ds_stride, _any_ptr(dx), _code(dx), dx_stride, _ptr(dh, None), _ptr(dgate, None),
+        _ptr(dres, None), _ptr(dw_post), _ptr(dscale), _ptr(dw_pre), eps, N, D, _wptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream)),
         "pararnn_block_norm_adjoint")
 
 
 def _rows(t, name, shape, dev):
-    """Row stride in elements of a [..., D] tensor whose leading axes make up
-    one axis of rows (0 for None)."""
+    """(pointer, type code, row stride in elements) of a [..., D] tensor whose
+    leading axes make up one axis of rows (None -> NULL)."""
     if t is None:
-        return 0
+        return None, 0, 0
     if t.device != dev or t.shape != shape:
         raise ValueError(f"{name}: expected {tuple(shape)} on {dev}, got {tuple(t.shape)} on {t.device}")
+    if t.is_contiguous():
+        return t.data_ptr(), _code(t), shape[-1]
     st = t.stride()
     if st[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}: channels must be contiguous")
@@ -727,21 +739,24 @@ def _rows(t, name, shape, dev):
         elif s != ld * rows:
             raise ValueError(f"{name}: rows must lie at one stride")
         rows *= n
-    return shape[-1] if ld is None else ld
+    return t.data_ptr(), _code(t), shape[-1] if ld is None else ld
 
 
 def _norm_parts(h, gate, act, w_post, res, scale, w_pre):
+    """(device, shape, rows, channels, the library's arguments from h to w_pre)"""
     dev = _first(h, "h")
     shape = h.shape
-    if h.dim() < 1 or h.numel() == 0:
+    if not shape or h.numel() == 0:
         raise PararnnError(-1, f"block norm of shape {tuple(shape)}")
-    if act not in _ACTS:
+    kind = _ACTS.get(act)
+    if kind is None:
         raise ValueError(f"act: expected one of {sorted(_ACTS)}, got {act!r}")
     D = shape[-1]
-    for t, name in ((w_post, "w_post"), (scale, "scale"), (w_pre, "w_pre")):
-        _need(t, name, (D,), dev)
-    return (dev, shape, h.numel() // D, D, _rows(h, "h", shape, dev), _rows(gate, "gate", shape, dev),
-            _rows(res, "res", shape, dev))
+    w = (D,)
+    return (dev, shape, h.numel() // D, D,
+            (*_rows(h, "h", shape, dev), *_rows(gate, "gate", shape, dev), kind,
+             _need(w_post, "w_post", w, dev), *_rows(res, "res", shape, dev),
+             _need(scale, "scale", w, dev), _need(w_pre, "w_pre", w, dev)))
 
 
 def block_norm(h, *, gate=None, act="silu", w_post=None, res=None, scale=None, w_pre=None, eps=1e-6,
@@ -757,17 +772,18 @@ def block_norm(h, *, gate=None, act="silu", w_post=None, res=None, scale=None, w
     bf16 or fp32; they and h may be views whose rows lie at one stride (a
     multiple of 8 elements).  `out` = (s, x), either None for a new tensor; s
     may be res (in-place update)."""
-    dev, shape, N, D, lh, lg, lr = _norm_parts(h, gate, act, w_post, res, scale, w_pre)
+    dev, shape, N, D, parts = _norm_parts(h, gate, act, w_post, res, scale, w_pre)
     s, x = out or (None, None)
-    _need(s, "s", shape, dev, (torch.float32, torch.bfloat16))
-    _need(x, "x", shape, dev, (torch.float32, torch.bfloat16))
+    sp, xp = _need(s, "s", shape, dev, _FLOATS), _need(x, "x", shape, dev, _FLOATS)
     with _on(dev, stream):
         if s is None and (want_s or w_pre is None):
-            s = torch.empty(shape, device=dev, dtype=s_dtype or (torch.bfloat16 if res is None
-                                                                 else res.dtype))
+            s = h.new_empty(shape, dtype=s_dtype or (_BF16 if res is None else res.dtype))
+            sp = s.data_ptr()
         if x is None and w_pre is not None:
-            x = torch.empty(shape, dtype=x_dtype, device=dev)
-        pararnn_block_norm(h, lh, gate, lg, _ACTS[act], w_post, res, lr, scale, w_pre, s, x, eps, N, D)
+            x = h.new_empty(shape, dtype=x_dtype)
+            xp = x.data_ptr()
+        _check(load_library().pararnn_block_norm(*parts, sp, _code(s), xp, _code(x), eps, N, D,
+                                                 _raw_stream(dev.index)), "pararnn_block_norm")
     return s, x
 
 
@@ -778,18 +794,19 @@ def block_norm_adjoint(h, ds, dx, *, gate=None, act="silu", w_post=None, res=Non
     the types of h, gate, res) and dw_post, dscale, dw_pre [D] fp32, None
     where the part is absent.  h, gate and res hold what the forward call
     read."""
-    dev, shape, N, D, lh, lg, lr = _norm_parts(h, gate, act, w_post, res, scale, w_pre)
+    dev, shape, N, D, parts = _norm_parts(h, gate, act, w_post, res, scale, w_pre)
     if (dx is None) != (w_pre is None):
         raise ValueError("dx: given exactly when w_pre is")
-    lds, ldx = _rows(ds, "ds", shape, dev), _rows(dx, "dx", shape, dev)
+    given = (*_rows(ds, "ds", shape, dev), *_rows(dx, "dx", shape, dev))
     with _on(dev, stream):
         def like(t):
-            return None if t is None else torch.empty(shape, dtype=t.dtype, device=dev)
-        def sums(t):
-            return None if t is None else torch.empty((D,), dtype=torch.float32, device=dev)
-        dh, dg, dr = like(h), like(gate), like(res)
-        dwp, dsc, dwq = sums(w_post), sums(scale), sums(w_pre)
-        ws = torch.empty(max(256, pararnn_block_norm_workspace_size(N, D)), dtype=torch.uint8, device=dev)
-        pararnn_block_norm_adjoint(h, lh, gate, lg, _ACTS[act], w_post, res, lr, scale, w_pre, ds, lds,
-                                   dx, ldx, dh, dg, dr, dwp, dsc, dwq, eps, N, D, ws)
-    return {"dh": dh, "dgate": dg, "dres": dr, "dw_post": dwp, "dscale": dsc, "dw_pre": dwq}
+            return None if t is None else t.new_empty(shape)
+        outs = [like(h), like(gate), like(res)]
+        outs += [None if t is None else torch.empty_like(t) for t in (w_post, scale, w_pre)]
+        lib = load_library()
+        nbytes = max(256, lib.pararnn_block_norm_workspace_size(N, D))
+        ws = h.new_empty(nbytes, dtype=torch.uint8)
+        _check(lib.pararnn_block_norm_adjoint(*parts, *given, *map(_any_ptr, outs), eps, N, D,
+                                              ws.data_ptr(), nbytes, _raw_stream(dev.index)),
+               "pararnn_block_norm_adjoint")
+    return dict(zip(("dh", "dgate", "dres", "dw_post", "dscale", "dw_pre"), outs))

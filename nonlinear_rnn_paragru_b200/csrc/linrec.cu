@@ -171,6 +171,17 @@ __device__ __forceinline__ unsigned lin_marks(const unsigned char* at, int dir, 
   return bits;
 }
 
+// Whether a warp's steps have no reset; and f(whether they may), so that the
+// rounds without one, which are most, pay nothing for it.
+__device__ __forceinline__ bool no_marks(unsigned resets) { return __all_sync(0xffffffffu, resets == 0u); }
+template <bool kReset, typename F>
+__device__ __forceinline__ void by_marks(unsigned resets, F f) {
+  if (kReset && !no_marks(resets))
+    f(std::true_type());
+  else
+    f(std::false_type());
+}
+
 // Shape of a scan kernel: GL lanes of a group, W warps, K steps of a thread in
 // a round, a ring of S rounds, at least R CTAs on an SM.
 template <int CELL, bool kBF16>
@@ -262,16 +273,19 @@ __global__ void __launch_bounds__(32 * FwdShape<CELL, kBF16>::W, FwdShape<CELL, 
     // steps past T compute on what the ring holds there: nothing after them is
     // stored
     float2 P[K], Q[K];  // h after step j is P[j] h_in + Q[j]
+    auto compose = [&](auto marked) {
 #pragma unroll
-    for (int j = 0; j < K; ++j) {
-      float2 u[G], nm, bb;
+      for (int j = 0; j < K; ++j) {
+        float2 u[G], nm, bb;
 #pragma unroll
-      for (int q = 0; q < G; ++q) u[q] = row_pair<kBF16>(rows + (j * G + q) * U::kRow, gl);
-      cell.coef(u, nm, bb);
-      P[j] = j ? lfma(nm, P[j - 1], P[j - 1]) : ladd(nm, both(1.f));
-      Q[j] = j ? lin_step(nm, bb, Q[j - 1]) : bb;
-      if (kReset && ((resets >> j) & 1u)) Q[j] = bb;
-    }
+        for (int q = 0; q < G; ++q) u[q] = row_pair<kBF16>(rows + (j * G + q) * U::kRow, gl);
+        cell.coef(u, nm, bb);
+        P[j] = j ? lfma(nm, P[j - 1], P[j - 1]) : ladd(nm, both(1.f));
+        Q[j] = j ? lin_step(nm, bb, Q[j - 1]) : bb;
+        if (decltype(marked)::value && ((resets >> j) & 1u)) Q[j] = bb;
+      }
+    };
+    by_marks<kReset>(resets, compose);
     float4 map = make_float4(P[K - 1].x, P[K - 1].y, Q[K - 1].x, Q[K - 1].y);
     if (kReset && resets) map.x = map.y = -1.f;
     const float2 in = lin_exchange<W, GL, kReset>(sh, cta, nround, map, rank, CL, carry, lost);
@@ -400,24 +414,27 @@ __global__ void __launch_bounds__(32 * BwdShape<CELL, kBF16>::W, BwdShape<CELL, 
     slot = slot + 1 == S ? 0 : slot + 1;
     // lambda of step j is L[j] + P[j] mu, mu what comes from the steps after
     float2 nm[K], L[K], P[K], keep[K][Cell::kKeep], mu = both(0.f), pr = both(1.f);
+    auto compose = [&](auto marked) {
 #pragma unroll
-    for (int j = 0; j < K; ++j) {
-      cell.head(row_pair<kBF16>(urows + j * G * U::kRow, gl), nm[j], keep[j]);
-      L[j] = ladd(row_pair<false>(grows + j * F::kRow, gl), mu);
-      P[j] = pr;
-      mu = lfma(nm[j], L[j], L[j]);
-      pr = lfma(nm[j], pr, pr);
-      if (kReset && ((resets >> j) & 1u)) mu = pr = both(0.f);
-    }
+      for (int j = 0; j < K; ++j) {
+        cell.head(row_pair<kBF16>(urows + j * G * U::kRow, gl), nm[j], keep[j]);
+        L[j] = ladd(row_pair<false>(grows + j * F::kRow, gl), mu);
+        P[j] = pr;
+        mu = lfma(nm[j], L[j], L[j]);
+        pr = lfma(nm[j], pr, pr);
+        if (decltype(marked)::value && ((resets >> j) & 1u)) mu = pr = both(0.f);
+      }
+    };
+    by_marks<kReset>(resets, compose);
     if (kReset && resets) pr = both(-1.f);
     mu = lin_exchange<W, GL, kReset>(sh, cta, nround, make_float4(pr.x, pr.y, mu.x, mu.y), rank, CL, carry, lost);
     float2 add[G + 1];
 #pragma unroll
     for (int q = 0; q <= G; ++q) add[q] = both(0.f);
-    auto step = [&](int j, bool first_step) {
+    auto step = [&](int j, bool first_step, bool marked) {
       float2 lt = lfma(P[j], mu, L[j]);
-      if (kReset && (resets & ((1u << j) - 1u))) lt = L[j];  // nothing of mu comes before a reset
-      const bool rs = kReset && ((resets >> j) & 1u);
+      if (marked && (resets & ((1u << j) - 1u))) lt = L[j];  // nothing of mu comes before a reset
+      const bool rs = marked && ((resets >> j) & 1u);
       float2 hp = row_pair<false>(hrows + j * F::kRow, gl);
       if (first_step) {
         hp = vec2(p.h0 ? p.h0 + (size_t)b * p.D : nullptr, d);
@@ -444,13 +461,13 @@ __global__ void __launch_bounds__(32 * BwdShape<CELL, kBF16>::W, BwdShape<CELL, 
       }
       if (CELL == PARARNN_LIN_DECAY) add[G] = ladd(add[G], e);
     };
-    if (t1 > K) {
+    if (t1 > K && (!kReset || no_marks(resets))) {
 #pragma unroll
-      for (int j = 0; j < K; ++j) step(j, false);
-    } else {
+      for (int j = 0; j < K; ++j) step(j, false, false);
+    } else {  // a round with resets, or the sequence's first steps
 #pragma unroll
       for (int j = 0; j < K; ++j)
-        if (t1 - 1 - j >= 0) step(j, t1 - 1 - j == 0);
+        if (t1 - 1 - j >= 0) step(j, t1 - 1 - j == 0, kReset);
     }
     du_at -= (long long)round * (long long)(G * pairs);
     // a round's sums first, then the running sums: over long sequences the

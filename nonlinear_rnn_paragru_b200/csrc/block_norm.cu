@@ -412,13 +412,18 @@ __global__ void __launch_bounds__(512) norm_bwd(const NormParams p, const int tp
   if (kNarrow || threadIdx.x == 0)
     for (int k = 0; k < S - 1; ++k) copy(row + k * step, k);
   float kh1 = 1.f;  // 1 / rms(h) of the row at hand
-  auto first_norm = [&](unsigned r) {
-    wait(r, 0);
-    float q[6] = {squares(0), 0.f, 0.f, 0.f, 0.f, 0.f};
+  auto first_norm = [&](unsigned r, int k) {
+    wait(r, k);
+    float q[6] = {squares(k), 0.f, 0.f, 0.f, 0.f, 0.f};
     row_sum6<kNarrow>(q, tpr, sh, buf);
     kh1 = rsqrtf(fmaf(q[0], invD, p.eps));
   };
-  if (post && S > 1) first_norm(0);
+  // The next row's h^2 can only join this row's exchange where the next row is
+  // on its way before it: with three slots, as the one freed by an exchange takes
+  // the row S - 1 ahead (narrow rows are copied before it).  Else a row has an
+  // exchange of its own for it.
+  const bool join = kNarrow || S >= 3;
+  if (post && join) first_norm(0, 0);
   int at = 0;  // slot of the row at hand
   unsigned nr = 0;
   for (long long r0 = (long long)blockIdx.x * slots; r0 < p.N; r0 += step, row += step, ++nr) {
@@ -429,11 +434,10 @@ __global__ void __launch_bounds__(512) norm_bwd(const NormParams p, const int tp
       __syncthreads();
       if (threadIdx.x == 0) copy(row, 0);
     }
-    if (S == 1 && post) first_norm(nr);
+    if (post && !join) first_norm(nr, at);
     wait(nr, at);
-    const bool ahead = post && S > 1 && row + step < p.N;
+    const bool ahead = post && join && row + step < p.N;
     if (!kNarrow && ahead) wait(nr + 1, next);
-    if (lost) kh1 = __int_as_float(0x7fffffff);
     const float2 kh = both(kh1);
     float q[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     F8 hh[NV], s[NV];
@@ -470,7 +474,7 @@ __global__ void __launch_bounds__(512) norm_bwd(const NormParams p, const int tp
     const float k1 = pre ? rsqrtf(fmaf(q[0], invD, p.eps)) : 0.f, nm1 = -(q[1] * k1 * invD);
     const float2 k = both(k1), nmean = both(nm1);
     const float2 nmean3 = both(-(fmaf(k1, fmaf(k1 * nm1, q[4], q[3]), q[2]) * invD));
-    if (post) kh1 = rsqrtf(fmaf(q[5], invD, p.eps));
+    if (post && join) kh1 = rsqrtf(fmaf(q[5], invD, p.eps));
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = 8 * (i * tpr + t);
@@ -485,6 +489,7 @@ __global__ void __launch_bounds__(512) norm_bwd(const NormParams p, const int tp
         ap[i].v[j] = lfma(dx.v[j], sn, ap[i].v[j]);
         d.v[j] = lfma(k, lfma(sn, nmean, lmul(dx.v[j], w.v[j])), d.v[j]);
       }
+      if (lost) d = {both(__int_as_float(0x7fffffff)), d.v[1], d.v[2], d.v[3]};
       if (p.dres && ok) store8(p.dres, row * p.D + c, f32<TP>(p, kR32), d);
       if (gate) {
         const F8 g = get(tg, kG32, i, at);

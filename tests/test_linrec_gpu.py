@@ -49,7 +49,7 @@ def adjoint(cell, x, h, **kw):
 
 def check_states(h, H, E, what=""):
     err = np.abs(h.cpu().numpy().astype(np.float64) - H)
-    bad = err > E + 1e-37
+    bad = ~(err <= E + 1e-37)   # a NaN is off too
     assert not bad.any(), (what, float((err / (E + 1e-37)).max()), np.argwhere(bad)[:3])
 
 
@@ -57,7 +57,7 @@ def check_adjoint(got, want, rounded):
     for k, (v, e) in want.items():
         g = got[k].double().cpu().numpy()
         tol = e + 1e-37 + (HALF * (np.abs(v) + e) if k == "du" and rounded else 0)
-        bad = np.abs(g - v) > tol
+        bad = ~(np.abs(g - v) <= tol)
         assert not bad.any(), (k, float((np.abs(g - v) / tol).max()), np.argwhere(bad)[:3])
 
 

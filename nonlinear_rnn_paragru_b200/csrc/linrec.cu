@@ -183,18 +183,24 @@ __device__ __forceinline__ void by_marks(unsigned resets, F f) {
 }
 
 // Shape of a scan kernel: GL lanes of a group, W warps, K steps of a thread in
-// a round, a ring of S rounds, at least R CTAs on an SM.
-template <int CELL, bool kBF16>
+// a round, a ring of S rounds, at least R CTAs on an SM.  More steps a round
+// mean fewer exchanges, but more registers and shared memory, so fewer CTAs on
+// an SM for the sequence to be split over.
+//   kTall    the longest rounds that leave two to four CTAs on an SM
+//   kShort   LIN_GRU with bf16 u: 8 steps, five CTAs, taken where that lets the
+//            cluster grow (300 tiles of 2048 steps: 70 us against 83; 128 tiles
+//            of 4096 steps: 64 against 61)
+//   kNarrow  tiles of 16 channels, for problems of so few 64-channel tiles that
+//            clusters of 8 CTAs leave SMs idle (one tile of 16384 steps: 18 us
+//            against 54; 16 tiles of 65536 steps: 191 against 249)
+enum Variant { kTall, kShort, kNarrow };
+template <int CELL, bool kBF16, int V>
 struct FwdShape {
   static constexpr bool kGru = CELL == PARARNN_LIN_GRU;
-#ifdef FG
-  static constexpr int GL = FG, W = FW, K = FK, S = FS, R = FR;
-#else
-  static constexpr int GL = 32, W = 4;
-  static constexpr int K = !kBF16 ? 16 : kGru ? 8 : 12;
-  static constexpr int S = kGru ? 3 : 2;
-  static constexpr int R = !kBF16 ? 2 : kGru ? 5 : 4;
-#endif
+  static constexpr int GL = V == kNarrow ? 8 : 32, W = V == kNarrow ? 8 : 4;
+  static constexpr int K = V == kShort ? 8 : V == kTall && kBF16 && !kGru ? 12 : 16;
+  static constexpr int S = V == kShort || (V == kTall && !kBF16 && kGru) ? 3 : 2;
+  static constexpr int R = V == kNarrow ? (kBF16 ? 2 : 1) : V == kShort ? 5 : kBF16 ? 4 : 2;
   using U = Rows<GL, K, LinCell<CELL>::G, kBF16 ? 2 : 4>;
   static constexpr int kWarp = S * U::kRound;   // bytes of a warp's ring
   static constexpr int kBytes = W * kWarp;
@@ -206,11 +212,11 @@ __device__ __forceinline__ float2 row_pair(const char* row, int lane) {
   return *reinterpret_cast<const float2*>(row + 8 * lane);
 }
 
-template <int CELL, bool kBF16, bool kReset>
-__global__ void __launch_bounds__(32 * FwdShape<CELL, kBF16>::W, FwdShape<CELL, kBF16>::R)
+template <int CELL, bool kBF16, int V, bool kReset>
+__global__ void __launch_bounds__(32 * FwdShape<CELL, kBF16, V>::W, FwdShape<CELL, kBF16, V>::R)
     linrec_fwd(const LinParams p, const int CL) {
   using Cell = LinCell<CELL>;
-  using Shape = FwdShape<CELL, kBF16>;
+  using Shape = FwdShape<CELL, kBF16, V>;
   using U = typename Shape::U;
   constexpr int G = Cell::G, K = Shape::K, W = Shape::W, S = Shape::S, GL = Shape::GL, ES = kBF16 ? 2 : 4;
   constexpr int KW = U::kNG * K;  // steps of a warp in a round
@@ -310,13 +316,11 @@ __global__ void __launch_bounds__(32 * FwdShape<CELL, kBF16>::W, FwdShape<CELL, 
 
 // Reverse scan: lambda_t = g_t + mu_{t+1}, mu_t = (1 - m_t) lambda_t (0 at a
 // reset, and mu_1 = dL/dh0).  Positions run from the last step to the first.
-template <int CELL, bool kBF16>
+// (kTall with fp32 u: 8 steps, 12 do not leave two CTAs on an SM)
+template <int CELL, bool kBF16, int V>
 struct BwdShape {
-#ifdef BG
-  static constexpr int GL = BG, W = BW, K = BK, S = BS, R = BR;
-#else
-  static constexpr int GL = 32, W = 4, K = kBF16 ? 12 : 8, S = 2, R = 2;
-#endif
+  static constexpr int GL = V == kNarrow ? 8 : 32, W = V == kNarrow ? 8 : 4;
+  static constexpr int K = V == kTall && kBF16 ? 12 : 8, S = 2, R = V == kNarrow ? 1 : 2;
   using U = Rows<GL, K, LinCell<CELL>::G, kBF16 ? 2 : 4>;
   using F = Rows<GL, K, 1, 4>;
   static constexpr int kH = U::kRound, kG = kH + F::kRound;  // offsets of h_{t-1} and dL/dh in a round
@@ -325,11 +329,11 @@ struct BwdShape {
   static constexpr int kBytes = W * kWarp;
 };
 
-template <int CELL, bool kBF16, bool kBF16Out, bool kReset>
-__global__ void __launch_bounds__(32 * BwdShape<CELL, kBF16>::W, BwdShape<CELL, kBF16>::R)
+template <int CELL, bool kBF16, bool kBF16Out, int V, bool kReset>
+__global__ void __launch_bounds__(32 * BwdShape<CELL, kBF16, V>::W, BwdShape<CELL, kBF16, V>::R)
     linrec_bwd(const LinParams p, const int CL) {
   using Cell = LinCell<CELL>;
-  using Shape = BwdShape<CELL, kBF16>;
+  using Shape = BwdShape<CELL, kBF16, V>;
   using U = typename Shape::U;
   using F = typename Shape::F;
   constexpr int G = Cell::G, K = Shape::K, W = Shape::W, S = Shape::S, GL = Shape::GL, ES = kBF16 ? 2 : 4;
@@ -461,7 +465,8 @@ __global__ void __launch_bounds__(32 * BwdShape<CELL, kBF16>::W, BwdShape<CELL, 
       }
       if (CELL == PARARNN_LIN_DECAY) add[G] = ladd(add[G], e);
     };
-    if (t1 > K && (!kReset || no_marks(resets))) {
+    const bool clean = !kReset || no_marks(resets);  // asked by the whole warp: t1 differs between its groups
+    if (t1 > K && clean) {
 #pragma unroll
       for (int j = 0; j < K; ++j) step(j, false, false);
     } else {  // a round with resets, or the sequence's first steps
@@ -563,37 +568,58 @@ int launch_scan(Kern kern, int GL, int threads, int smem, LinParams p, int CL, c
   return (int)cudaLaunchKernelEx(&cfg, kern, p, CL);
 }
 
-// CTAs of a cluster: as many as fill one wave of `per_sm` CTAs on 148 SMs, no
-// more than the sequence has rounds of one CTA (`steps`) for.
-int cluster_for(int B, int T, int D, int GL, int per_sm, int steps) {
-  const long long tiles = (long long)B * ((D + 2 * GL - 1) / (2 * GL));
+long long tiles_of(int B, int D, int GL) { return (long long)B * ((D + 2 * GL - 1) / (2 * GL)); }
+
+// clusters of 8 on 64-channel tiles would not fill 148 SMs
+bool few_tiles(int B, int D) { return tiles_of(B, D, 32) * kLinMaxCluster <= 148; }
+
+// CTAs of a cluster: as many as fill one wave of H::R CTAs on each of 148 SMs,
+// no more than the sequence has rounds of one CTA for.
+template <typename H>
+int cluster_of(int B, int T, int D) {
+  const long long tiles = tiles_of(B, D, H::GL);
   int CL = 1;
-  while (CL < kLinMaxCluster && 2 * tiles * CL <= 148 * per_sm && T > CL * steps) CL *= 2;
+  while (CL < kLinMaxCluster && 2 * tiles * CL <= 148 * H::R && T > CL * H::W * H::U::kNG * H::K) CL *= 2;
   return CL;
+}
+
+template <int CELL, bool kBF16, int V>
+int launch_fwd_v(const LinParams& p, cudaStream_t stream) {
+  using H = FwdShape<CELL, kBF16, V>;
+  const int CL = cluster_of<H>(p.B, p.T, p.D);
+  return p.reset ? launch_scan(linrec_fwd<CELL, kBF16, V, true>, H::GL, 32 * H::W, H::kBytes, p, CL, stream)
+                 : launch_scan(linrec_fwd<CELL, kBF16, V, false>, H::GL, 32 * H::W, H::kBytes, p, CL, stream);
 }
 
 template <int CELL, bool kBF16>
 int launch_fwd_t(const LinParams& p, cudaStream_t stream) {
-  using H = FwdShape<CELL, kBF16>;
-  const int CL = cluster_for(p.B, p.T, p.D, H::GL, H::R, H::W * H::U::kNG * H::K);
-  return p.reset ? launch_scan(linrec_fwd<CELL, kBF16, true>, H::GL, 32 * H::W, H::kBytes, p, CL, stream)
-                 : launch_scan(linrec_fwd<CELL, kBF16, false>, H::GL, 32 * H::W, H::kBytes, p, CL, stream);
+  if (few_tiles(p.B, p.D)) return launch_fwd_v<CELL, kBF16, kNarrow>(p, stream);
+  if constexpr (CELL == PARARNN_LIN_GRU && kBF16)
+    if (cluster_of<FwdShape<CELL, true, kShort>>(p.B, p.T, p.D) > cluster_of<FwdShape<CELL, true, kTall>>(p.B, p.T, p.D))
+      return launch_fwd_v<CELL, true, kShort>(p, stream);
+  return launch_fwd_v<CELL, kBF16, kTall>(p, stream);
 }
 
 // the same for both types of u, so that the workspace does not depend on it
 template <int CELL>
 int bwd_cluster(int B, int T, int D) {
-  using H = BwdShape<CELL, true>;
-  static_assert(H::GL == BwdShape<CELL, false>::GL, "one tile width");
-  return cluster_for(B, T, D, H::GL, H::R, H::W * H::U::kNG * H::K);
+  return few_tiles(B, D) ? cluster_of<BwdShape<CELL, true, kNarrow>>(B, T, D)
+                         : cluster_of<BwdShape<CELL, true, kTall>>(B, T, D);
+}
+
+template <int CELL, bool kBF16, bool kBF16Out, int V>
+int launch_bwd_v(const LinParams& p, cudaStream_t stream) {
+  using H = BwdShape<CELL, kBF16, V>;
+  const int CL = bwd_cluster<CELL>(p.B, p.T, p.D);
+  return p.reset
+             ? launch_scan(linrec_bwd<CELL, kBF16, kBF16Out, V, true>, H::GL, 32 * H::W, H::kBytes, p, CL, stream)
+             : launch_scan(linrec_bwd<CELL, kBF16, kBF16Out, V, false>, H::GL, 32 * H::W, H::kBytes, p, CL, stream);
 }
 
 template <int CELL, bool kBF16, bool kBF16Out>
 int launch_bwd_t(const LinParams& p, cudaStream_t stream) {
-  using H = BwdShape<CELL, kBF16>;
-  const int CL = bwd_cluster<CELL>(p.B, p.T, p.D);
-  return p.reset ? launch_scan(linrec_bwd<CELL, kBF16, kBF16Out, true>, H::GL, 32 * H::W, H::kBytes, p, CL, stream)
-                 : launch_scan(linrec_bwd<CELL, kBF16, kBF16Out, false>, H::GL, 32 * H::W, H::kBytes, p, CL, stream);
+  return few_tiles(p.B, p.D) ? launch_bwd_v<CELL, kBF16, kBF16Out, kNarrow>(p, stream)
+                             : launch_bwd_v<CELL, kBF16, kBF16Out, kTall>(p, stream);
 }
 
 template <int CELL>

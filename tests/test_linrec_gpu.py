@@ -65,7 +65,10 @@ def check_adjoint(got, want, rounded):
 # rounds; one lane pair, a partial tile, several tiles
 SHAPES = [(1, 1, 8), (3, 1, 200), (1, 2, 64), (2, 7, 72), (1, 8, 64), (1, 9, 8), (5, 63, 24), (1, 64, 64),
           (1, 65, 128), (2, 129, 200), (1, 500, 1000), (3, 1531, 136), (1, 4099, 64), (7, 33, 520),
-          (300, 3, 72)]
+          (300, 3, 72),
+          # tiles enough for the wide kernels: clusters of 8, 4, 2 and 1, rounds
+          # that end inside a group, a warp and a CTA
+          (20, 700, 72), (1, 600, 2048), (38, 260, 136), (150, 70, 200), (30, 150, 640), (10, 129, 1000)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])

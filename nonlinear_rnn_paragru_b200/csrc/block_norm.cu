@@ -15,6 +15,7 @@
 #include <utility>
 
 #include "block_norm.cuh"
+#include "colsum.cuh"
 #include "linrec_cell.cuh"
 
 namespace pararnn {
@@ -523,55 +524,35 @@ __global__ void __launch_bounds__(512) norm_bwd(const NormParams p, const int tp
   }
   if (kNarrow) asm volatile("cp.async.wait_group 0;" ::: "memory");
   if (!p.part) return;
-  float* const out = p.part + (size_t)blockIdx.x * 3 * p.D;
+  // [blocks][parts with a weight][D]: w_post, scale, w_pre
+  const int n = (post ? 1 : 0) + (scale ? 1 : 0) + (pre ? 1 : 0);
+  float* const out = p.part + (size_t)blockIdx.x * n * p.D;
   if (!kNarrow) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = 8 * (i * tpr + t);
       if (c >= p.D) continue;
-      store8(out + c, 0, true, aw[i]);
-      store8(out + p.D + c, 0, true, as[i]);
-      store8(out + 2 * (size_t)p.D + c, 0, true, ap[i]);
+      float* q = out + c;
+      if (post) store8(q, 0, true, aw[i]), q += p.D;
+      if (scale) store8(q, 0, true, as[i]), q += p.D;
+      if (pre) store8(q, 0, true, ap[i]);
     }
     return;
   }
   // several rows a block: its slots' sums, in their order
-  float* const acc = reinterpret_cast<float*>(smem);  // [3][slots x 8 tpr]: 2048 channels each (256 threads of 8)
+  float* const acc = reinterpret_cast<float*>(smem);  // [n][slots x 8 tpr]: 2048 channels each (256 threads of 8)
   const int width = 8 * tpr;
   __syncthreads();
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    float* q = acc + slot * width + 8 * t + 2 * j;
-    q[0] = aw[0].v[j].x, q[1] = aw[0].v[j].y;
-    q[2048] = as[0].v[j].x, q[2049] = as[0].v[j].y;
-    q[4096] = ap[0].v[j].x, q[4097] = ap[0].v[j].y;
-  }
+  float* q = acc + slot * width + 8 * t;
+  if (post) store8(q, 0, true, aw[0]), q += 2048;
+  if (scale) store8(q, 0, true, as[0]), q += 2048;
+  if (pre) store8(q, 0, true, ap[0]);
   __syncthreads();
-  for (int i = threadIdx.x; i < 3 * p.D; i += blockDim.x) {
+  for (int i = threadIdx.x; i < n * p.D; i += blockDim.x) {
     const int k = i / p.D, c = i - k * p.D;
     float v = 0.f;
     for (int s = 0; s < slots; ++s) v += acc[k * 2048 + s * width + c];
     out[i] = v;
-  }
-}
-
-// Column sums of part [P][3][D] into up to three [D] vectors, in a fixed order.
-__global__ void __launch_bounds__(256) norm_colsum(const float* __restrict__ part, int P, int D, float* o0,
-                                                   float* o1, float* o2) {
-  __shared__ float s[8][33];
-  const int x = threadIdx.x & 31, y = threadIdx.x >> 5, c = blockIdx.x * 32 + x;
-  float* const out = blockIdx.y == 0 ? o0 : blockIdx.y == 1 ? o1 : o2;
-  if (!out) return;  // the whole block
-  float v = 0.f;
-  if (c < D)
-#pragma unroll 4
-    for (int i = y; i < P; i += 8) v += part[((size_t)i * 3 + blockIdx.y) * D + c];
-  s[y][x] = v;
-  __syncthreads();
-  if (y == 0 && c < D) {
-#pragma unroll
-    for (int i = 1; i < 8; ++i) v += s[i][x];
-    out[c] = v;
   }
 }
 
@@ -601,7 +582,7 @@ int norm_blocks(long long N, const NormShape& s, int sm_threads) {
   const long long most = 148 * std::max(1, sm_threads / s.threads);
   return (int)std::min<long long>((N + s.slots() - 1) / s.slots(), most);
 }
-constexpr int kFwdThreads = 1024, kBwdThreads = 512;
+constexpr int kFwdThreads = 1024, kBwdThreads = 512, kBwdMost = 1024;
 
 // The canonical type bits: those of absent tensors follow the others, so that
 // they do not take a call off its kernel.
@@ -629,21 +610,21 @@ void launch_fwd_t(const NormParams& p, int types, int blocks, const NormShape& s
 // leave room for the blocks that the registers allow on an SM (one for five
 // fp32 tensors of nearly 8192 channels).  The slots' sums of several rows a
 // block lie where the ring was.
-int bwd_ring(const NormParams& p, const NormShape& s, int& S) {
+int bwd_ring(const NormParams& p, const NormShape& s, int sm_threads, int& S) {
   int es = 0;
   for (auto [on, bit] : {std::pair<bool, int>{true, kH32}, {p.parts & kGate, kG32},
                          {(p.parts & kRes) && (p.parts & kPre), kR32}, {p.parts & kDs, kS32}, {p.parts & kPre, kX32}})
     if (on) es += p.types & bit ? 4 : 2;
-  const int row = (s.slots() > 1 ? 8 * s.threads : p.D) * es, room = 220 * 1024 / std::max(1, kBwdThreads / s.threads);
+  const int row = (s.slots() > 1 ? 8 * s.threads : p.D) * es, room = 220 * 1024 / std::max(1, sm_threads / s.threads);
   S = 4;
   while (S > 1 && S * row > room) --S;
   return std::max(S * row, s.slots() > 1 ? 3 * 2048 * 4 : 0);
 }
 
 template <int NV, bool kNarrow, int TP, int PT>
-int launch_bwd_k(const NormParams& p, int blocks, const NormShape& s, cudaStream_t stream) {
+int launch_bwd_k(const NormParams& p, int sm_threads, const NormShape& s, cudaStream_t stream) {
   int S;
-  const int smem = bwd_ring(p, s, S);
+  const int smem = bwd_ring(p, s, sm_threads, S), blocks = norm_blocks(p.N, s, sm_threads);
   cudaError_t e = cudaFuncSetAttribute(norm_bwd<NV, kNarrow, TP, PT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return (int)e;
   norm_bwd<NV, kNarrow, TP, PT><<<blocks, s.threads, smem, stream>>>(p, s.tpr, S);
@@ -655,27 +636,27 @@ int launch_bwd_k(const NormParams& p, int blocks, const NormShape& s, cudaStream
 constexpr int kPartsPre = kPre | kRes | kDs, kPartsPost = kPost | kGate | kDs,
               kPartsBoth = kPost | kGate | kRes | kPre | kDs, kPartsAll = kPartsBoth | kScale;
 template <int TP>
-int launch_bwd_t(const NormParams& p, int blocks, const NormShape& s, cudaStream_t stream) {
+int launch_bwd_t(const NormParams& p, int sm_threads, const NormShape& s, cudaStream_t stream) {
   switch (p.parts) {
-    case kPartsPre: return launch_bwd_k<1, false, TP, kPartsPre>(p, blocks, s, stream);
-    case kPartsPost: return launch_bwd_k<1, false, TP, kPartsPost>(p, blocks, s, stream);
-    case kPartsBoth: return launch_bwd_k<1, false, TP, kPartsBoth>(p, blocks, s, stream);
-    case kPartsAll: return launch_bwd_k<1, false, TP, kPartsAll>(p, blocks, s, stream);
-    default: return launch_bwd_k<1, false, TP, kAnyPart>(p, blocks, s, stream);
+    case kPartsPre: return launch_bwd_k<1, false, TP, kPartsPre>(p, sm_threads, s, stream);
+    case kPartsPost: return launch_bwd_k<1, false, TP, kPartsPost>(p, sm_threads, s, stream);
+    case kPartsBoth: return launch_bwd_k<1, false, TP, kPartsBoth>(p, sm_threads, s, stream);
+    case kPartsAll: return launch_bwd_k<1, false, TP, kPartsAll>(p, sm_threads, s, stream);
+    default: return launch_bwd_k<1, false, TP, kAnyPart>(p, sm_threads, s, stream);
   }
 }
-int launch_bwd(const NormParams& p, int blocks, const NormShape& s, cudaStream_t stream) {
+int launch_bwd(const NormParams& p, int sm_threads, const NormShape& s, cudaStream_t stream) {
   if (s.nv == 2)
-    return p.types == kH32 && p.parts == kPartsAll ? launch_bwd_k<2, false, kH32, kPartsAll>(p, blocks, s, stream)
-                                                   : launch_bwd_k<2, false, kAnyType, kAnyPart>(p, blocks, s, stream);
-  if (s.slots() > 1) return launch_bwd_k<1, true, kAnyType, kAnyPart>(p, blocks, s, stream);
+    return p.types == kH32 && p.parts == kPartsAll ? launch_bwd_k<2, false, kH32, kPartsAll>(p, sm_threads, s, stream)
+                                                   : launch_bwd_k<2, false, kAnyType, kAnyPart>(p, sm_threads, s, stream);
+  if (s.slots() > 1) return launch_bwd_k<1, true, kAnyType, kAnyPart>(p, sm_threads, s, stream);
   switch (p.types) {
-    case 0: return launch_bwd_t<0>(p, blocks, s, stream);
-    case kH32: return launch_bwd_t<kH32>(p, blocks, s, stream);
-    case kR32 | kS32: return launch_bwd_t<kR32 | kS32>(p, blocks, s, stream);
-    case kH32 | kR32 | kS32: return launch_bwd_t<kH32 | kR32 | kS32>(p, blocks, s, stream);
-    case 31: return launch_bwd_t<31>(p, blocks, s, stream);
-    default: return launch_bwd_k<1, false, kAnyType, kAnyPart>(p, blocks, s, stream);
+    case 0: return launch_bwd_t<0>(p, sm_threads, s, stream);
+    case kH32: return launch_bwd_t<kH32>(p, sm_threads, s, stream);
+    case kR32 | kS32: return launch_bwd_t<kR32 | kS32>(p, sm_threads, s, stream);
+    case kH32 | kR32 | kS32: return launch_bwd_t<kH32 | kR32 | kS32>(p, sm_threads, s, stream);
+    case 31: return launch_bwd_t<31>(p, sm_threads, s, stream);
+    default: return launch_bwd_k<1, false, kAnyType, kAnyPart>(p, sm_threads, s, stream);
   }
 }
 
@@ -684,7 +665,7 @@ int launch_bwd(const NormParams& p, int blocks, const NormShape& s, cudaStream_t
 int norm_max_d() { return kNormMaxD; }
 
 size_t norm_part_floats(long long N, int D) {
-  return (size_t)norm_blocks(N, norm_shape(D), kBwdThreads) * 3 * D;
+  return (size_t)norm_blocks(N, norm_shape(D), kBwdMost) * 3 * D;
 }
 
 int launch_norm_fwd(const NormParams& p, cudaStream_t stream) {
@@ -699,15 +680,22 @@ int launch_norm_fwd(const NormParams& p, cudaStream_t stream) {
 
 int launch_norm_bwd(NormParams p, float* dw_post, float* dscale, float* dw_pre, cudaStream_t stream) {
   const NormShape s = norm_shape(p.D);
-  const int blocks = norm_blocks(p.N, s, kBwdThreads);
   p.types = canonical_types(p, p.ds, p.dx);
   p.parts = (p.w_post ? kPost : 0) | (p.g ? kGate : 0) | (p.res ? kRes : 0) | (p.scale ? kScale : 0) |
             (p.w_pre ? kPre : 0) | (p.ds ? kDs : 0);
+  // threads that an SM's registers hold: more where fewer parts leave more
+  const int sm_threads = p.D <= 256 || p.D > 4096 ? kBwdThreads
+                         : p.parts == kPartsPre   ? kBwdMost
+                         : p.parts == kPartsPost  ? 640
+                                                  : kBwdThreads;
   if (!dw_post && !dscale && !dw_pre) p.part = nullptr;
-  const int e = launch_bwd(p, blocks, s, stream);
+  const int e = launch_bwd(p, sm_threads, s, stream);
   if (e || !p.part) return e;
-  norm_colsum<<<dim3((p.D + 31) / 32, 3), 256, 0, stream>>>(p.part, blocks, p.D, dw_post, dscale, dw_pre);
-  return (int)cudaGetLastError();
+  ColSums sums = {p.part, norm_blocks(p.N, s, sm_threads), 0, p.D, {}};
+  if (p.w_post) sums.out[sums.n++] = dw_post;
+  if (p.scale) sums.out[sums.n++] = dscale;
+  if (p.w_pre) sums.out[sums.n++] = dw_pre;
+  return launch_colsum(sums, stream);
 }
 
 }  // namespace pararnn

@@ -21,6 +21,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "colsum.cuh"
 #include "linrec_cell.cuh"
 
 namespace cg = cooperative_groups;
@@ -484,42 +485,20 @@ __global__ void __launch_bounds__(32 * BwdShape<CELL, kBF16, V>::W, BwdShape<CEL
   if (!p.part) return;
   if (CELL == PARARNN_LIN_DECAY) sum[G] = lmul(sum[G], Cell::lam_scale(p.lam, d));
   // the groups' sums, in their order
+  constexpr int NS = CELL == PARARNN_LIN_DECAY ? G + 1 : G;
   __syncthreads();
-  float2* const acc = reinterpret_cast<float2*>(ring);  // [G + 1][W * 32]
-  static_assert(Shape::kBytes >= W * (G + 1) * 32 * (int)sizeof(float2), "sums fit");
-  static_assert(W > G, "a warp for each sum");
+  float2* const acc = reinterpret_cast<float2*>(ring);  // [NS][W * 32]
+  static_assert(Shape::kBytes >= W * NS * 32 * (int)sizeof(float2), "sums fit");
+  static_assert(W >= NS, "a warp for each sum");
 #pragma unroll
-  for (int q = 0; q <= G; ++q) acc[q * W * 32 + threadIdx.x] = sum[q];
+  for (int q = 0; q < NS; ++q) acc[q * W * 32 + threadIdx.x] = sum[q];
   __syncthreads();
-  if (warp <= G && lane < GL && live) {
+  if (warp < NS && lane < GL && live) {
     float2 s = both(0.f);
     for (int i = 0; i < W * 32 / GL; ++i) s = ladd(s, acc[warp * W * 32 + i * GL + lane]);
-    float* q = p.part + ((size_t)(b * CL + rank) * (G + 1) + warp) * p.D + d;
+    float* q = p.part + ((size_t)(b * CL + rank) * NS + warp) * p.D + d;
     q[0] = s.x;
     q[1] = s.y;
-  }
-}
-
-// Sums of the rows of part [P][C], in a fixed order: 32 columns a block, 8
-// threads a column.  Columns [0, c1) go to out1, the rest to out2 (either may
-// be NULL).
-__global__ void __launch_bounds__(256) linrec_colsum(const float* __restrict__ part, int P, int C, int c1,
-                                                     float* out1, float* out2) {
-  __shared__ float s[8][33];
-  const int x = threadIdx.x & 31, y = threadIdx.x >> 5, c = blockIdx.x * 32 + x;
-  float v = 0.f;
-  if (c < C)
-    for (int i = y; i < P; i += 8) v += part[(size_t)i * C + c];
-  s[y][x] = v;
-  __syncthreads();
-  if (y == 0 && c < C) {
-#pragma unroll
-    for (int i = 1; i < 8; ++i) v += s[i][x];
-    if (c < c1) {
-      if (out1) out1[c] = v;
-    } else if (out2) {
-      out2[c - c1] = v;
-    }
   }
 }
 
@@ -638,7 +617,7 @@ int linrec_bwd_cluster(int cell, int B, int T, int D) {
 long long linrec_most_ctas(int B, int D) { return (long long)B * (D / 8) * kLinMaxCluster; }
 
 size_t linrec_part_floats(int cell, int B, int T, int D) {
-  return (size_t)B * linrec_bwd_cluster(cell, B, T, D) * (cell == PARARNN_LIN_GRU ? 3 : 4) * D;
+  return (size_t)B * linrec_bwd_cluster(cell, B, T, D) * (cell == PARARNN_LIN_GRU ? 2 : 4) * D;
 }
 
 int launch_linrec_fwd(int cell, bool bf16, const LinParams& p, cudaStream_t stream) {
@@ -654,10 +633,10 @@ int launch_linrec_bwd(int cell, bool bf16, bool bf16_out, LinParams p, float* dl
                                   : launch_bwd_c<PARARNN_LIN_DECAY>(bf16, bf16_out, p, stream);
   if (e || !p.part) return e;
   const int G = cell == PARARNN_LIN_GRU ? 2 : 3;
-  const int C = (G + 1) * p.D;
-  linrec_colsum<<<(C + 31) / 32, 256, 0, stream>>>(p.part, p.B * linrec_bwd_cluster(cell, p.B, p.T, p.D), C,
-                                                   G * p.D, dbias, dlam);
-  return (int)cudaGetLastError();
+  ColSums sums = {p.part, p.B * linrec_bwd_cluster(cell, p.B, p.T, p.D), cell == PARARNN_LIN_GRU ? G : G + 1, p.D, {}};
+  for (int q = 0; q < G; ++q) sums.out[q] = dbias ? dbias + (size_t)q * p.D : nullptr;
+  if (cell == PARARNN_LIN_DECAY) sums.out[G] = dlam;
+  return launch_colsum(sums, stream);
 }
 
 int launch_linrec_step(int cell, bool bf16, const LinParams& p, const float* h_prev, float* h_next,

@@ -218,7 +218,7 @@ struct LinParams {
   const float* g;        // dL/dh
   void* du;
   float* dh0;
-  float* part;           // adjoint: [B * CL][(G + 1) D] sums over a CTA's steps
+  float* part;           // adjoint: [B * CL][G or, with dlam, G + 1][D] sums over a CTA's steps
   int B, T, D;
   int ntd;               // tiles of a batch row (set at the launch)
 };

@@ -152,6 +152,7 @@ int pararnn_linrec_step(int cell, const void* u_t, int u_dtype, long long u_stri
   const int rc = lin_args(cell, u_t, u_dtype, u_stride_b, 0, u_stride_g, lam, bias, B, 1, D, kappa);
   if (rc) return rc;
   if (!h_next) return PARARNN_ERR_INVALID_ARG;
+  if ((long long)B * D >= (1LL << 38)) return PARARNN_ERR_TOO_LARGE;
   if ((h_prev && !aligned(h_prev, 4)) || !aligned(h_next, 4)) return PARARNN_ERR_MISALIGNED;
   const LinParams p = lin_params(u_t, u_stride_b, 0, u_stride_g, lam, bias, nullptr, nullptr, B, 1, D, kappa);
   return done(launch_linrec_step(cell, u_dtype == PARARNN_BF16, p, h_prev, h_next, (cudaStream_t)stream));

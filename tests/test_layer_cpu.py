@@ -200,6 +200,7 @@ def _host_cases():
     step("cell", -1, cell=9)
     step("no_out", -1, hn=None)
     step("D4", -1, D=4)
+    step("too_large", -6, B=1 << 30, D=1 << 8)
     step("out_misaligned", -5, hn=0x3002)
     step("prev_misaligned", -5, hp=0x3001)
 

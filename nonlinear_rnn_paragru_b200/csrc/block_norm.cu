@@ -683,11 +683,14 @@ int launch_norm_bwd(NormParams p, float* dw_post, float* dscale, float* dw_pre, 
   p.types = canonical_types(p, p.ds, p.dx);
   p.parts = (p.w_post ? kPost : 0) | (p.g ? kGate : 0) | (p.res ? kRes : 0) | (p.scale ? kScale : 0) |
             (p.w_pre ? kPre : 0) | (p.ds ? kDs : 0);
-  // threads that an SM's registers hold: more where fewer parts leave more
-  const int sm_threads = p.D <= 256 || p.D > 4096 ? kBwdThreads
-                         : p.parts == kPartsPre   ? kBwdMost
-                         : p.parts == kPartsPost  ? 640
-                                                  : kBwdThreads;
+  // threads that an SM's registers hold: more where fewer parts leave more, and
+  // its shared memory still holds a row ahead (a third with a first norm)
+  int sm_threads = kBwdThreads, S;
+  if (p.D > 256 && p.D <= 4096 && (p.parts == kPartsPre || p.parts == kPartsPost)) {
+    const int more = p.parts == kPartsPre ? kBwdMost : 640;
+    bwd_ring(p, s, more, S);
+    if (S >= (p.parts == kPartsPost ? 3 : 2)) sm_threads = more;
+  }
   if (!dw_post && !dscale && !dw_pre) p.part = nullptr;
   const int e = launch_bwd(p, sm_threads, s, stream);
   if (e || !p.part) return e;

@@ -63,6 +63,8 @@ KINDS = {
     "post_gate": dict(gate=BF16, post=True), "full": FULL,
     "full_f32": dict(gate=F32, post=True, res=F32, scale=True, pre=True, x=F32),
     "gate": dict(gate=F32, s=F32), "scale_res": dict(h=BF16, scale=True, res=BF16), "none": dict(s=F32),
+    "both": dict(gate=BF16, post=True, res=F32, pre=True), "pre_f32": dict(h=F32, res=F32, pre=True, x=F32),
+    "mixed": dict(h=BF16, gate=F32, post=True, res=BF16, scale=True, pre=True, s=F32, x=F32),
     "post_f32_out": dict(h=BF16, post=True, s=F32), "gate_scale_pre": dict(gate=BF16, scale=True, pre=True),
 }
 
@@ -79,11 +81,22 @@ def test_widths_match_the_oracle(cuda_ok, D):
 
 
 @pytest.mark.parametrize("kind,D", [("full_f32", 4096), ("full_f32", 5600), ("full_f32", 8192), ("full", 8192),
-                                    ("full", 4096), ("post_gate", 8192), ("res_pre", 8192)])
+                                    ("full", 4096), ("post_gate", 8192), ("res_pre", 8192), ("post_gate", 1000),
+                                    ("res_pre", 1000), ("res_pre", 4096), ("pre_f32", 4096), ("pre_f32", 520),
+                                    ("both", 1000), ("mixed", 1000), ("full_f32", 776), ("full", 136)])
 def test_wide_rows_of_several_rounds(cuda_ok, kind, D):
     # more rows than blocks, at the widths where the adjoint's ring holds four
     # rows, three, two and one
-    check(*draw(330, D, **KINDS[kind], seed=D))
+    check(*draw(330 if D > 600 else 1300, D, **KINDS[kind], seed=D))
+
+
+def test_only_one_of_the_gradients(cuda_ok):
+    p, d, st, xt = draw(700, 520, **FULL)
+    for ds, dx, w in ((None, d["dx"], p["w_pre"]), (d["ds"], None, None)):
+        q = {**p, "w_pre": w}
+        got = pr.block_norm_adjoint(ds=ds, dx=dx, **q)
+        for k, (v, m) in ol.block_norm_adjoint(ds=ds, dx=dx, **q).items():
+            close(got[k], v, m, 700 * 2.0 ** -24 if v.ndim == 1 else 0.0, what=k)
 
 
 @pytest.mark.parametrize("N", [1, 2, 8, 9, 147, 1000, 5000])

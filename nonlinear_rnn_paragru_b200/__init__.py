@@ -652,24 +652,36 @@ def linrec_adjoint(cell, u, lam, bias, h0, h, dLdh, *, reset=None, kappa=8.0, wa
     if h is None or dLdh is None:
         raise ValueError("h and dLdh are needed")
     sp, gp = _need(h, "h", (B, T, D), dev), _need(dLdh, "dLdh", (B, T, D), dev)
-    o = out or {}
+    du = dlam = dbias = dh0 = None
+    if out:
+        du, dlam, dbias, dh0 = (out.get(k) for k in ("du", "dlam", "dbias", "dh0"))
+        _need(du, "du", (B, T, G, D), dev, _FLOATS)
+        _need(dlam, "dlam", (D,), dev)
+        _need(dbias, "dbias", (G, D), dev)
+        _need(dh0, "dh0", (B, D), dev)
+    lib = load_library()
     with _on(dev, stream):
-        def new(name, shape, dtype=_F32, dtypes=(_F32,)):
-            t = o.get(name)
-            if t is None:
-                t = u.new_empty(shape, dtype=dtype)
-                return t, t.data_ptr()
-            return t, _need(t, name, shape, dev, dtypes)
-        du, dup = new("du", (B, T, G, D), du_dtype or u.dtype, _FLOATS)
-        dlam, dlp = new("dlam", (D,)) if want_params and lam is not None else (None, None)
-        dbias, dbp = new("dbias", (G, D)) if want_params else (None, None)
-        dh0, dhp = new("dh0", (B, D)) if want_dh0 else (None, None)
-        lib = load_library()
+        if du is None:
+            du = u.new_empty((B, T, G, D), dtype=du_dtype or u.dtype)
+        if not want_params:
+            dlam = dbias = None
+        else:
+            if lam is None:
+                dlam = None
+            elif dlam is None:
+                dlam = torch.empty_like(lam)
+            if dbias is None:
+                dbias = u.new_empty((G, D), dtype=_F32)
+        if not want_dh0:
+            dh0 = None
+        elif dh0 is None:
+            dh0 = u.new_empty((B, D), dtype=_F32)
         nbytes = max(256, lib.pararnn_linrec_workspace_size(cell, B, T, D))
         ws = u.new_empty(nbytes, dtype=torch.uint8)
         _check(lib.pararnn_linrec_adjoint(
-            cell, u.data_ptr(), _code(u), *st, lp, bp, hp, rp, sp, gp, dup, _code(du), dlp, dbp, dhp,
-            B, T, D, kappa, ws.data_ptr(), nbytes, _raw_stream(dev.index)), "pararnn_linrec_adjoint")
+            cell, u.data_ptr(), _code(u), *st, lp, bp, hp, rp, sp, gp, du.data_ptr(), _code(du),
+            _any_ptr(dlam), _any_ptr(dbias), _any_ptr(dh0), B, T, D, kappa, ws.data_ptr(), nbytes,
+            _raw_stream(dev.index)), "pararnn_linrec_adjoint")
     return {"du": du, "dlam": dlam, "dbias": dbias, "dh0": dh0}
 
 

@@ -625,8 +625,9 @@ template <int NV, bool kNarrow, int TP, int PT>
 int launch_bwd_k(const NormParams& p, int sm_threads, const NormShape& s, cudaStream_t stream) {
   int S;
   const int smem = bwd_ring(p, s, sm_threads, S), blocks = norm_blocks(p.N, s, sm_threads);
-  cudaError_t e = cudaFuncSetAttribute(norm_bwd<NV, kNarrow, TP, PT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return (int)e;
+  static SmemOnce once;
+  const int e = once.allow(reinterpret_cast<const void*>(norm_bwd<NV, kNarrow, TP, PT>), smem);
+  if (e) return e;
   norm_bwd<NV, kNarrow, TP, PT><<<blocks, s.threads, smem, stream>>>(p, s.tpr, S);
   return (int)cudaGetLastError();
 }

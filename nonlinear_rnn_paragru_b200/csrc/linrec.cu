@@ -527,11 +527,11 @@ __global__ void __launch_bounds__(256) linrec_step(const LinParams p, const floa
 }
 
 template <typename Kern>
-int launch_scan(Kern kern, int GL, int threads, int smem, LinParams p, int CL, cudaStream_t stream) {
+int launch_scan(Kern kern, int GL, int threads, int smem, LinParams p, int CL, SmemOnce& once, cudaStream_t stream) {
   p.ntd = (p.D + 2 * GL - 1) / (2 * GL);
+  const int e = once.allow(reinterpret_cast<const void*>(kern), smem + 2 * kLinMaxCluster * GL * 16);
+  if (e) return e;
   if (CL > 1) smem += 2 * CL * GL * 16;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return (int)e;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(threads);
   cfg.gridDim = dim3((unsigned)((long long)p.B * p.ntd * CL));
@@ -565,9 +565,11 @@ int cluster_of(int B, int T, int D) {
 template <int CELL, bool kBF16, int V>
 int launch_fwd_v(const LinParams& p, cudaStream_t stream) {
   using H = FwdShape<CELL, kBF16, V>;
+  static SmemOnce once[2];
   const int CL = cluster_of<H>(p.B, p.T, p.D);
-  return p.reset ? launch_scan(linrec_fwd<CELL, kBF16, V, true>, H::GL, 32 * H::W, H::kBytes, p, CL, stream)
-                 : launch_scan(linrec_fwd<CELL, kBF16, V, false>, H::GL, 32 * H::W, H::kBytes, p, CL, stream);
+  return p.reset
+             ? launch_scan(linrec_fwd<CELL, kBF16, V, true>, H::GL, 32 * H::W, H::kBytes, p, CL, once[1], stream)
+             : launch_scan(linrec_fwd<CELL, kBF16, V, false>, H::GL, 32 * H::W, H::kBytes, p, CL, once[0], stream);
 }
 
 template <int CELL, bool kBF16>
@@ -589,10 +591,12 @@ int bwd_cluster(int B, int T, int D) {
 template <int CELL, bool kBF16, bool kBF16Out, int V>
 int launch_bwd_v(const LinParams& p, cudaStream_t stream) {
   using H = BwdShape<CELL, kBF16, V>;
+  static SmemOnce once[2];
   const int CL = bwd_cluster<CELL>(p.B, p.T, p.D);
-  return p.reset
-             ? launch_scan(linrec_bwd<CELL, kBF16, kBF16Out, V, true>, H::GL, 32 * H::W, H::kBytes, p, CL, stream)
-             : launch_scan(linrec_bwd<CELL, kBF16, kBF16Out, V, false>, H::GL, 32 * H::W, H::kBytes, p, CL, stream);
+  return p.reset ? launch_scan(linrec_bwd<CELL, kBF16, kBF16Out, V, true>, H::GL, 32 * H::W, H::kBytes, p, CL,
+                               once[1], stream)
+                 : launch_scan(linrec_bwd<CELL, kBF16, kBF16Out, V, false>, H::GL, 32 * H::W, H::kBytes, p, CL,
+                               once[0], stream);
 }
 
 template <int CELL, bool kBF16, bool kBF16Out>

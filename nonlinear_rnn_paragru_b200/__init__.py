@@ -526,15 +526,23 @@ def _need(t, name, shape, device, dtypes=(_F32,)):
     this device (None -> NULL)."""
     if t is None:
         return None
+    if t.shape == shape and t.dtype in dtypes and t.device == device and t.is_contiguous():
+        return t.data_ptr()
     if t.device != device:
         raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {t.dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous tensor")
-    return t.data_ptr()
+    raise ValueError(f"{name}: expected a contiguous tensor")
+
+
+def _like(t, shape, dtype, base):
+    """A new contiguous tensor: like `t` where that has its shape and type (the
+    cheaper call), else of `base`'s device."""
+    if t is not None and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return torch.empty_like(t)
+    return base.new_empty(shape, dtype=dtype)
 
 
 def _first(t, name):
@@ -662,7 +670,7 @@ def linrec_adjoint(cell, u, lam, bias, h0, h, dLdh, *, reset=None, kappa=8.0, wa
     lib = load_library()
     with _on(dev, stream):
         if du is None:
-            du = u.new_empty((B, T, G, D), dtype=du_dtype or u.dtype)
+            du = _like(u, u.shape, du_dtype or u.dtype, u)
         if not want_params:
             dlam = dbias = None
         else:
@@ -671,11 +679,11 @@ def linrec_adjoint(cell, u, lam, bias, h0, h, dLdh, *, reset=None, kappa=8.0, wa
             elif dlam is None:
                 dlam = torch.empty_like(lam)
             if dbias is None:
-                dbias = u.new_empty((G, D), dtype=_F32)
+                dbias = _like(bias, (G, D), _F32, u)
         if not want_dh0:
             dh0 = None
         elif dh0 is None:
-            dh0 = u.new_empty((B, D), dtype=_F32)
+            dh0 = _like(h0, (B, D), _F32, u)
         nbytes = max(256, lib.pararnn_linrec_workspace_size(cell, B, T, D))
         ws = u.new_empty(nbytes, dtype=torch.uint8)
         _check(lib.pararnn_linrec_adjoint(
@@ -789,10 +797,11 @@ def block_norm(h, *, gate=None, act="silu", w_post=None, res=None, scale=None, w
     sp, xp = _need(s, "s", shape, dev, _FLOATS), _need(x, "x", shape, dev, _FLOATS)
     with _on(dev, stream):
         if s is None and (want_s or w_pre is None):
-            s = h.new_empty(shape, dtype=s_dtype or (_BF16 if res is None else res.dtype))
+            s = _like(res if res is not None else h, shape,
+                      s_dtype or (_BF16 if res is None else res.dtype), h)
             sp = s.data_ptr()
         if x is None and w_pre is not None:
-            x = h.new_empty(shape, dtype=x_dtype)
+            x = _like(h, shape, x_dtype, h)
             xp = x.data_ptr()
         _check(load_library().pararnn_block_norm(*parts, sp, _code(s), xp, _code(x), eps, N, D,
                                                  _raw_stream(dev.index)), "pararnn_block_norm")
@@ -812,7 +821,7 @@ def block_norm_adjoint(h, ds, dx, *, gate=None, act="silu", w_post=None, res=Non
     given = (*_rows(ds, "ds", shape, dev), *_rows(dx, "dx", shape, dev))
     with _on(dev, stream):
         def like(t):
-            return None if t is None else t.new_empty(shape)
+            return None if t is None else _like(t, shape, t.dtype, t)
         outs = [like(h), like(gate), like(res)]
         outs += [None if t is None else torch.empty_like(t) for t in (w_post, scale, w_pre)]
         lib = load_library()

@@ -16,13 +16,11 @@ struct ColSums {
 // deep; then a warp folds a column (of 4 kDeep / 32 at a time).  32 deep, or 128
 // for so many partial sums that 32 threads wait for their loads (1184 of 1000
 // columns: 6 us against 13; of 16 of 4096 columns and three vectors the adjoint
-// takes 15 us with 128, 10 with 32).  Launched while the kernel before it still runs (its blocks wait for
-// that one's end here).
+// takes 15 us with 128, 10 with 32).
 template <int kDeep>
 __global__ void __launch_bounds__(8 * kDeep) colsum_kernel(const ColSums s) {
   __shared__ float4 part[kDeep][9];
   __shared__ float fold[32][33];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int x = threadIdx.x & 7, y = threadIdx.x >> 3, c = blockIdx.x * 32 + 4 * x;
   float* const out = s.out[blockIdx.y];
   if (!out) return;  // the whole block
@@ -54,17 +52,12 @@ __global__ void __launch_bounds__(8 * kDeep) colsum_kernel(const ColSums s) {
 }
 
 int launch_colsum(const ColSums& s, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((s.D + 31) / 32, s.n);
-  const bool deep = s.P > 320;
-  cfg.blockDim = dim3(deep ? 1024 : 256);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return (int)(deep ? cudaLaunchKernelEx(&cfg, colsum_kernel<128>, s) : cudaLaunchKernelEx(&cfg, colsum_kernel<32>, s));
+  const dim3 grid((s.D + 31) / 32, s.n);
+  if (s.P > 320)
+    colsum_kernel<128><<<grid, 1024, 0, stream>>>(s);
+  else
+    colsum_kernel<32><<<grid, 256, 0, stream>>>(s);
+  return (int)cudaGetLastError();
 }
 
 }  // namespace

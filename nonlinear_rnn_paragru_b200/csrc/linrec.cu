@@ -60,11 +60,12 @@ struct Rows {
 };
 
 // The groups' maps of a round, and the mbarriers that count the arrival of the
-// CTAs' maps; those lie in dynamic shared memory, 2 x CL x GL x 16 bytes.
+// CTAs' maps; those lie in dynamic shared memory, kLinBufs x CL x GL x 16 bytes.
+constexpr int kLinBufs = 4;
 template <int W>
 struct LinShared {
   float4 map[2][W * 32];
-  uint64_t bar[2];
+  uint64_t bar[kLinBufs];
 };
 
 __device__ __forceinline__ uint32_t map_rank(uint32_t addr, int rank) {
@@ -98,53 +99,70 @@ __device__ __forceinline__ float2 lin_join(const float4* cta, int rpos, int gl, 
   return in;
 }
 
-// Publish the thread's map of round r and return the state that enters its
-// steps; `carry`, the state that enters the round, becomes the one that leaves
-// it.  Positions (gpos of the group in the CTA, rpos of the CTA) run in the
-// order of the scan.  Buffers and mbarriers alternate: a CTA can only send the
-// maps of round r + 2 after every CTA's of round r + 1 came, which each sends
-// after all its warps have read those of round r.  The wait for the cluster is
-// bounded; where it runs out the states become NaN.
+// What a thread keeps of a round between its exchange and its end: the maps of
+// the CTA's steps before its own and, where the CTA is alone, of all its steps.
+struct LinTurn {
+  float4 before, all;
+};
+
+// Publish the thread's map of round r, and the CTA's to the cluster.  Positions
+// (gpos of the group in the CTA, rpos of the CTA) run in the order of the scan.
+// The groups' buffers alternate: round r + 2's are written after the barrier of
+// round r + 1, which each warp reaches after it read round r's.
 template <int W, int GL, bool kReset>
-__device__ __forceinline__ float2 lin_exchange(LinShared<W>& sh, float4* cta, unsigned r, float4 mine, int rpos,
-                                               int CL, float2& carry, bool& lost) {
+__device__ __forceinline__ LinTurn lin_publish(LinShared<W>& sh, float4* cta, unsigned r, float4 mine, int rpos,
+                                               int CL) {
   constexpr int NP = W * 32 / GL;
-  const int par = r & 1, gl = threadIdx.x % GL, gpos = threadIdx.x / GL;
-  sh.map[par][threadIdx.x] = mine;
+  const int gl = threadIdx.x % GL, gpos = threadIdx.x / GL;
+  sh.map[r & 1][threadIdx.x] = mine;
   __syncthreads();
-  const float4* maps = sh.map[par] + gl;
-  float2 in = carry;
-  if (CL == 1) {
+  const float4* maps = sh.map[r & 1] + gl;
+  LinTurn t;
+  t.before = make_float4(1.f, 1.f, 0.f, 0.f);
+  t.all = maps[0];
 #pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      if (i == gpos) in = carry;
-      carry = lin_apply<kReset>(maps[i * GL], carry);
-    }
-    return in;
-  }
-  float4 before = make_float4(1.f, 1.f, 0.f, 0.f);
-#pragma unroll
-  for (int i = 0; i < NP - 1; ++i) {
+  for (int i = 0; i < NP; ++i) {
     const float4 v = maps[i * GL];
-    if (i < gpos) before = i ? lin_then<kReset>(before, v) : v;
+    if (i < gpos) t.before = i ? lin_then<kReset>(t.before, v) : v;
+    if (i && CL == 1) t.all = lin_then<kReset>(t.all, v);
   }
-  if (gpos == NP - 1) {
-    const float4 all = lin_then<kReset>(before, mine);
-    if (gl == 0) mbar_arrive_expect_tx(&sh.bar[par], CL * GL * 16);
-    const uint32_t at = smem_u32(&cta[(par * CL + rpos) * GL + gl]), bar = smem_u32(&sh.bar[par]);
+  if (CL > 1 && gpos == NP - 1) {
+    const float4 all = lin_then<kReset>(t.before, mine);
+    const int buf = r % kLinBufs;
+    if (gl == 0) mbar_arrive_expect_tx(&sh.bar[buf], CL * GL * 16);
+    const uint32_t at = smem_u32(&cta[(buf * CL + rpos) * GL + gl]), bar = smem_u32(&sh.bar[buf]);
     for (int i = 0; i < CL; ++i) st_async16(map_rank(at, i), map_rank(bar, i), all);
   }
   __syncwarp();
-  if (!lost) lost = !mbar_wait_bounded(&sh.bar[par], (r >> 1) & 1, kLinWaitNs);
-  const float4* v = cta + par * CL * GL;
-  if (CL == 2)
-    in = lin_join<2, GL, kReset>(v, rpos, gl, carry);
-  else if (CL == 4)
-    in = lin_join<4, GL, kReset>(v, rpos, gl, carry);
-  else
-    in = lin_join<8, GL, kReset>(v, rpos, gl, carry);
-  if (lost) carry = in = both(__int_as_float(0x7fffffff));
-  return gpos ? lin_apply<kReset>(before, in) : in;
+  return t;
+}
+
+// The state that enters this thread's steps of round r; `carry`, which enters
+// the round, becomes what leaves it.  The CTAs' buffers are used in turn: a CTA
+// sends round r + 4's map after it ended round r + 2, for which it had every
+// CTA's map of that round, each sent after all its warps had ended round r
+// (rounds are published at most one ahead of their end).  The wait is bounded;
+// where it runs out the states become NaN.
+template <int W, int GL, bool kReset>
+__device__ __forceinline__ float2 lin_enter(LinShared<W>& sh, const float4* cta, unsigned r, const LinTurn& t,
+                                            int rpos, int CL, float2& carry, bool& lost) {
+  const int gl = threadIdx.x % GL, gpos = threadIdx.x / GL;
+  float2 in = carry;
+  if (CL == 1) {
+    carry = lin_apply<kReset>(t.all, carry);
+  } else {
+    const int buf = r % kLinBufs;
+    if (!lost) lost = !mbar_wait_bounded(&sh.bar[buf], (r / kLinBufs) & 1, kLinWaitNs);
+    const float4* v = cta + buf * CL * GL;
+    if (CL == 2)
+      in = lin_join<2, GL, kReset>(v, rpos, gl, carry);
+    else if (CL == 4)
+      in = lin_join<4, GL, kReset>(v, rpos, gl, carry);
+    else
+      in = lin_join<8, GL, kReset>(v, rpos, gl, carry);
+    if (lost) carry = in = both(__int_as_float(0x7fffffff));
+  }
+  return gpos ? lin_apply<kReset>(t.before, in) : in;
 }
 
 // Before the rounds: the mbarriers, and every CTA of the cluster runs before
@@ -153,7 +171,7 @@ template <int W>
 __device__ __forceinline__ void lin_cluster_start(LinShared<W>& sh, int CL) {
   if (CL == 1) return;
   if (threadIdx.x == 0)
-    for (int i = 0; i < 2; ++i) mbar_init(&sh.bar[i], 1);
+    for (int i = 0; i < kLinBufs; ++i) mbar_init(&sh.bar[i], 1);
   cg::this_cluster().sync();
 }
 
@@ -187,7 +205,12 @@ __device__ __forceinline__ void by_marks(unsigned resets, F f) {
 // a round, a ring of S rounds, at least R CTAs on an SM.  More steps a round
 // mean fewer exchanges, but more registers and shared memory, so fewer CTAs on
 // an SM for the sequence to be split over.
-//   kTall    the longest rounds that leave two to four CTAs on an SM
+//   kTall    the longest rounds that leave two to four CTAs on an SM.  With fp32
+//            u a round is published before the round before it ends (kAhead), so
+//            its exchange runs behind the next round's arithmetic, at twice the
+//            registers for maps: LIN_DECAY T65536 D2048 344 us against 422,
+//            LIN_GRU B8 T4096 D1024 66 against 70.  With bf16 the registers cost
+//            more CTAs than that gains (61 against 61 at best).
 //   kShort   LIN_GRU with bf16 u: 8 steps, five CTAs, taken where that lets the
 //            cluster grow (300 tiles of 2048 steps: 70 us against 83; 128 tiles
 //            of 4096 steps: 64 against 61)
@@ -199,9 +222,10 @@ template <int CELL, bool kBF16, int V>
 struct FwdShape {
   static constexpr bool kGru = CELL == PARARNN_LIN_GRU;
   static constexpr int GL = V == kNarrow ? 8 : 32, W = V == kNarrow ? 8 : 4;
-  static constexpr int K = V == kShort ? 8 : V == kTall && kBF16 && !kGru ? 12 : 16;
-  static constexpr int S = V == kShort || (V == kTall && !kBF16 && kGru) ? 3 : 2;
-  static constexpr int R = V == kNarrow ? (kBF16 ? 2 : 1) : V == kShort ? 5 : kBF16 ? 4 : 2;
+  static constexpr bool kAhead = V == kTall && !kBF16;
+  static constexpr int K = V == kNarrow ? 16 : V == kShort || (!kBF16 && kGru) ? 8 : kGru ? 16 : 12;
+  static constexpr int S = V == kShort ? 3 : 2;
+  static constexpr int R = V == kNarrow ? (kBF16 ? 2 : 1) : V == kShort ? 5 : kBF16 || kGru ? 4 : 2;
   using U = Rows<GL, K, LinCell<CELL>::G, kBF16 ? 2 : 4>;
   static constexpr int kWarp = S * U::kRound;   // bytes of a warp's ring
   static constexpr int kBytes = W * kWarp;
@@ -265,21 +289,25 @@ __global__ void __launch_bounds__(32 * FwdShape<CELL, kBF16, V>::W, FwdShape<CEL
   float2 carry = vec2(p.h0 ? p.h0 + (size_t)b * p.D : nullptr, d);
   const size_t row = (size_t)b * p.T;
   lin_cluster_start(sh, CL);
+  const int rounds = (p.T + round - 1) / round;
   bool lost = false;
   int slot = 0;
-  unsigned nround = 0;
-  for (int base = 0; base < p.T; base += round, ++nround) {
-    const int tw = base + first, t0 = tw + grp * K;
+  struct Round {
+    float2 P[K], Q[K];  // h after step j is P[j] h_in + Q[j]
+    unsigned resets;
+    LinTurn turn;
+  };
+  auto begin = [&](int r, Round& x) {  // round r's maps, published
+    const int tw = r * round + first, t0 = tw + grp * K;
     cp_async_wait<S - 2>();
     __syncwarp();
     copy(slot == 0 ? S - 1 : slot - 1);
     cp_async_commit();
-    const unsigned resets = kReset ? lin_marks<GL, K>(p.reset + row + t0, 1, p.T - t0) : 0u;
+    x.resets = kReset ? lin_marks<GL, K>(p.reset + row + t0, 1, p.T - t0) : 0u;
     const char* rows = mine + slot * U::kRound;
     slot = slot + 1 == S ? 0 : slot + 1;
     // steps past T compute on what the ring holds there: nothing after them is
     // stored
-    float2 P[K], Q[K];  // h after step j is P[j] h_in + Q[j]
     auto compose = [&](auto marked) {
 #pragma unroll
       for (int j = 0; j < K; ++j) {
@@ -287,29 +315,50 @@ __global__ void __launch_bounds__(32 * FwdShape<CELL, kBF16, V>::W, FwdShape<CEL
 #pragma unroll
         for (int q = 0; q < G; ++q) u[q] = row_pair<kBF16>(rows + (j * G + q) * U::kRow, gl);
         cell.coef(u, nm, bb);
-        P[j] = j ? lfma(nm, P[j - 1], P[j - 1]) : ladd(nm, both(1.f));
-        Q[j] = j ? lin_step(nm, bb, Q[j - 1]) : bb;
-        if (decltype(marked)::value && ((resets >> j) & 1u)) Q[j] = bb;
+        x.P[j] = j ? lfma(nm, x.P[j - 1], x.P[j - 1]) : ladd(nm, both(1.f));
+        x.Q[j] = j ? lin_step(nm, bb, x.Q[j - 1]) : bb;
+        if (decltype(marked)::value && ((x.resets >> j) & 1u)) x.Q[j] = bb;
       }
     };
-    by_marks<kReset>(resets, compose);
-    float4 map = make_float4(P[K - 1].x, P[K - 1].y, Q[K - 1].x, Q[K - 1].y);
-    if (kReset && resets) map.x = map.y = -1.f;
-    const float2 in = lin_exchange<W, GL, kReset>(sh, cta, nround, map, rank, CL, carry, lost);
+    by_marks<kReset>(x.resets, compose);
+    float4 map = make_float4(x.P[K - 1].x, x.P[K - 1].y, x.Q[K - 1].x, x.Q[K - 1].y);
+    if (kReset && x.resets) map.x = map.y = -1.f;
+    x.turn = lin_publish<W, GL, kReset>(sh, cta, r, map, rank, CL);
+  };
+  auto end = [&](int r, Round& x) {  // its states, stored
+    const int t0 = r * round + first + grp * K;
+    const float2 in = lin_enter<W, GL, kReset>(sh, cta, r, x.turn, rank, CL, carry, lost);
 #pragma unroll
     for (int j = 0; j < K; ++j) {
-      const float2 h = lfma(P[j], in, Q[j]);
-      if (!kReset || !(resets & ((2u << j) - 1u))) Q[j] = h;  // after a reset nothing is left of h_in
+      const float2 h = lfma(x.P[j], in, x.Q[j]);
+      if (!kReset || !(x.resets & ((2u << j) - 1u))) x.Q[j] = h;  // after a reset nothing is left of h_in
     }
     float* out = p.h + (row + t0) * p.D + d;
     if (t0 + K <= p.T) {
 #pragma unroll
       for (int j = 0; j < K; ++j)
-        if (live) *reinterpret_cast<float2*>(out + (size_t)j * p.D) = Q[j];
+        if (live) *reinterpret_cast<float2*>(out + (size_t)j * p.D) = x.Q[j];
     } else {
 #pragma unroll
       for (int j = 0; j < K; ++j)
-        if (live && t0 + j < p.T) *reinterpret_cast<float2*>(out + (size_t)j * p.D) = Q[j];
+        if (live && t0 + j < p.T) *reinterpret_cast<float2*>(out + (size_t)j * p.D) = x.Q[j];
+    }
+  };
+  Round x;
+  if constexpr (Shape::kAhead) {
+    Round y;
+    begin(0, x);
+    for (int r = 0; r < rounds; r += 2) {
+      if (r + 1 < rounds) begin(r + 1, y);
+      end(r, x);
+      if (r + 1 >= rounds) break;
+      if (r + 2 < rounds) begin(r + 2, x);
+      end(r + 1, y);
+    }
+  } else {
+    for (int r = 0; r < rounds; ++r) {
+      begin(r, x);
+      end(r, x);
     }
   }
   cp_async_wait<0>();
@@ -432,7 +481,9 @@ __global__ void __launch_bounds__(32 * BwdShape<CELL, kBF16, V>::W, BwdShape<CEL
     };
     by_marks<kReset>(resets, compose);
     if (kReset && resets) pr = both(-1.f);
-    mu = lin_exchange<W, GL, kReset>(sh, cta, nround, make_float4(pr.x, pr.y, mu.x, mu.y), rank, CL, carry, lost);
+    const LinTurn turn =
+        lin_publish<W, GL, kReset>(sh, cta, nround, make_float4(pr.x, pr.y, mu.x, mu.y), rank, CL);
+    mu = lin_enter<W, GL, kReset>(sh, cta, nround, turn, rank, CL, carry, lost);
     float2 add[G + 1];
 #pragma unroll
     for (int q = 0; q <= G; ++q) add[q] = both(0.f);
@@ -529,9 +580,9 @@ __global__ void __launch_bounds__(256) linrec_step(const LinParams p, const floa
 template <typename Kern>
 int launch_scan(Kern kern, int GL, int threads, int smem, LinParams p, int CL, SmemOnce& once, cudaStream_t stream) {
   p.ntd = (p.D + 2 * GL - 1) / (2 * GL);
-  const int e = once.allow(reinterpret_cast<const void*>(kern), smem + 2 * kLinMaxCluster * GL * 16);
+  const int e = once.allow(reinterpret_cast<const void*>(kern), smem + kLinBufs * kLinMaxCluster * GL * 16);
   if (e) return e;
-  if (CL > 1) smem += 2 * CL * GL * 16;
+  if (CL > 1) smem += kLinBufs * CL * GL * 16;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(threads);
   cfg.gridDim = dim3((unsigned)((long long)p.B * p.ntd * CL));

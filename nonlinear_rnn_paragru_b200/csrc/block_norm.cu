@@ -10,7 +10,12 @@
 // Blocks walk over rows: `tpr` threads a row of 8 NV channels each (a power of
 // two up to a warp for D <= 256, several rows a block; else the whole block),
 // and a thread loads its share of the next row before it works on this one, so
-// that HBM stays busy through the row's two or three sums.
+// that HBM stays busy through the row's two sums.
+//
+// Measured (B200, warm): all parts, fp32 states, the rest bf16: N32768 D1024
+// forward 65.5 us (403 MB: 6.1 TB/s, held by HBM), adjoint 140 us; N8192 D4096
+// adjoint 145 us (671 MB: 4.6 TB/s), held by the latency of a row's phases in the
+// one block that the registers (weights and their sums: 48) leave an SM.
 #include <algorithm>
 #include <utility>
 

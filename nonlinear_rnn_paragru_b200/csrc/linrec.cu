@@ -180,8 +180,8 @@ __device__ __forceinline__ void lin_cluster_start(LinShared<W>& sh, int CL) {
   cg::this_cluster().sync();
 }
 
-// A group's marked steps: bit j for its j-th step of the scan, `step` of which
-// is at reset[at + dir * j], `n` of them within the sequence.
+// A group's marked steps: bit j for its j-th step in the order of the scan, whose
+// mark lies at at[dir * j]; `n` of the steps are within the sequence.
 template <int GL, int K>
 __device__ __forceinline__ unsigned lin_marks(const unsigned char* at, int dir, int n) {
   const int gl = threadIdx.x % GL, shift = threadIdx.x % 32 / GL * GL;
@@ -220,8 +220,8 @@ __device__ __forceinline__ void by_marks(unsigned resets, F f) {
 //            cluster grow (300 tiles of 2048 steps: 70 us against 83; 128 tiles
 //            of 4096 steps: 64 against 61)
 //   kNarrow  tiles of 16 channels, for problems of so few 64-channel tiles that
-//            clusters of 8 CTAs leave SMs idle (one tile of 16384 steps: 18 us
-//            against 54; 16 tiles of 65536 steps: 191 against 249)
+//            clusters of 8 CTAs leave SMs idle (one tile of 16384 steps: 17 us
+//            against 54; 16 tiles of 65536 steps: 169 against 249)
 enum Variant { kTall, kShort, kNarrow };
 template <int CELL, bool kBF16, int V>
 struct FwdShape {

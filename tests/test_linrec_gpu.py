@@ -68,7 +68,7 @@ SHAPES = [(1, 1, 8), (3, 1, 200), (1, 2, 64), (2, 7, 72), (1, 8, 64), (1, 9, 8),
           (300, 3, 72),
           # tiles enough for the wide kernels: clusters of 8, 4, 2 and 1, rounds
           # that end inside a group, a warp and a CTA
-          (20, 700, 72), (1, 600, 2048), (38, 260, 136), (150, 70, 200), (30, 150, 640), (10, 129, 1000), (1, 3000, 1216)]
+          (20, 700, 72), (1, 602, 2048), (38, 260, 136), (150, 70, 200), (30, 150, 640), (10, 129, 1000), (1, 2999, 1216)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])

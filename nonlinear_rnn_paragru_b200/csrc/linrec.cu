@@ -180,20 +180,33 @@ __device__ __forceinline__ void lin_cluster_start(LinShared<W>& sh, int CL) {
   cg::this_cluster().sync();
 }
 
-// A group's marked steps: bit j for its j-th step in the order of the scan, whose
-// mark lies at at[dir * j]; `n` of the steps are within the sequence.
+// A group's marks: its j-th step in the order of the scan has its mark at
+// at[dir * j], `n` of the steps are within the sequence.  A lane loads those of
+// steps gl, gl + GL, ... (a round before they are asked for, so that no round
+// waits for them), and the vote makes them bits of the group's steps.
 template <int GL, int K>
-__device__ __forceinline__ unsigned lin_marks(const unsigned char* at, int dir, int n) {
-  const int gl = threadIdx.x % GL, shift = threadIdx.x % 32 / GL * GL;
-  unsigned bits = 0;
+struct Marks {
+  static constexpr int M = (K + GL - 1) / GL;
+  unsigned char raw[M];
+  __device__ __forceinline__ void load(const unsigned char* at, int dir, int n) {
+    const int gl = threadIdx.x % GL;
 #pragma unroll
-  for (int m = 0; m < K; m += GL) {
-    const bool mark = gl + m < min(K, n) && at[(long long)dir * (gl + m)] != 0;
-    const unsigned all = __ballot_sync(0xffffffffu, mark) >> shift;
-    bits |= (GL == 32 ? all : all & ((1u << (GL % 32)) - 1u)) << m;
+    for (int m = 0; m < M; ++m) {
+      raw[m] = 0;
+      if (gl + m * GL < min(K, n)) raw[m] = at[(long long)dir * (gl + m * GL)];
+    }
   }
-  return bits;
-}
+  __device__ __forceinline__ unsigned vote() const {
+    const int shift = threadIdx.x % 32 / GL * GL;
+    unsigned bits = 0;
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      const unsigned all = __ballot_sync(0xffffffffu, raw[m] != 0) >> shift;
+      bits |= (GL == 32 ? all : all & ((1u << (GL % 32)) - 1u)) << (m * GL);
+    }
+    return bits;
+  }
+};
 
 // Whether a warp's steps have no reset; and f(whether they may), so that the
 // rounds without one, which are most, pay nothing for it.
@@ -302,13 +315,19 @@ __global__ void __launch_bounds__(32 * FwdShape<CELL, kBF16, V>::W, FwdShape<CEL
     unsigned resets;
     LinTurn turn;
   };
+  Marks<GL, K> marks;
+  if (kReset) marks.load(p.reset + row + first + grp * K, 1, p.T - first - grp * K);
   auto begin = [&](int r, Round& x) {  // round r's maps, published
-    const int tw = r * round + first, t0 = tw + grp * K;
+    const int t0 = r * round + first + grp * K;
     cp_async_wait<S - 2>();
     __syncwarp();
     copy(slot == 0 ? S - 1 : slot - 1);
     cp_async_commit();
-    x.resets = kReset ? lin_marks<GL, K>(p.reset + row + t0, 1, p.T - t0) : 0u;
+    x.resets = 0u;
+    if (kReset) {
+      x.resets = marks.vote();
+      marks.load(p.reset + row + t0 + round, 1, p.T - t0 - round);
+    }
     const char* rows = mine + slot * U::kRound;
     slot = slot + 1 == S ? 0 : slot + 1;
     // steps past T compute on what the ring holds there: nothing after them is
@@ -460,13 +479,19 @@ __global__ void __launch_bounds__(32 * BwdShape<CELL, kBF16, V>::W, BwdShape<CEL
   using Out = typename std::conditional<kBF16Out, __nv_bfloat162, float2>::type;
   const size_t pairs = p.D / 2;  // channel pairs of a row of du
   Out* du_at = static_cast<Out*>(p.du) + ((long long)row + p.T - 1 - first - grp * K) * (long long)(G * pairs) + d / 2;
+  Marks<GL, K> marks;
+  if (kReset) marks.load(p.reset + row + p.T - 1 - first - grp * K, -1, p.T - first - grp * K);
   for (int end = p.T; end > 0; end -= round, ++nround) {
     const int t1 = end - first - grp * K;  // this thread's steps: t1 - 1, ..., t1 - K
     cp_async_wait<S - 2>();
     __syncwarp();
     copy(slot == 0 ? S - 1 : slot - 1);
     cp_async_commit();
-    const unsigned resets = kReset ? lin_marks<GL, K>(p.reset + row + t1 - 1, -1, t1) : 0u;
+    unsigned resets = 0u;
+    if (kReset) {
+      resets = marks.vote();
+      marks.load(p.reset + row + t1 - 1 - round, -1, t1 - round);
+    }
     const char* urows = umine + slot * Shape::kRound;
     const char* grows = fmine + slot * Shape::kRound + Shape::kG;
     const char* hrows = fmine + slot * Shape::kRound + Shape::kH;

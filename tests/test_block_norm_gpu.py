@@ -83,11 +83,12 @@ def test_widths_match_the_oracle(cuda_ok, D):
 @pytest.mark.parametrize("kind,D", [("full_f32", 4096), ("full_f32", 5600), ("full_f32", 8192), ("full", 8192),
                                     ("full", 4096), ("post_gate", 8192), ("res_pre", 8192), ("post_gate", 1000),
                                     ("res_pre", 1000), ("res_pre", 4096), ("pre_f32", 4096), ("pre_f32", 520),
-                                    ("both", 1000), ("mixed", 1000), ("full_f32", 776), ("full", 136)])
+                                    ("both", 1000), ("mixed", 1000), ("full_f32", 776), ("full", 136), ("post_gate", 136),
+                                    ("res_pre", 72), ("full_f32", 200), ("both", 24), ("mixed", 256)])
 def test_wide_rows_of_several_rounds(cuda_ok, kind, D):
     # more rows than blocks, at the widths where the adjoint's ring holds four
     # rows, three, two and one
-    check(*draw(330 if D > 600 else 1300, D, **KINDS[kind], seed=D))
+    check(*draw(330 if D > 600 else 1300 if D > 256 else 6000, D, **KINDS[kind], seed=D))
 
 
 def test_only_one_of_the_gradients(cuda_ok):

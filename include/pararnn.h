@@ -510,6 +510,22 @@ int pararnn_linrec_solve(int cell, const void* u, int u_dtype,
                          const unsigned char* reset, float* h, int B, int T,
                          int D, float kappa, pararnn_stream_t stream);
 
+/* pararnn_linrec_solve with options and a status word.  *status (device int,
+ * NULL to skip) receives 0, or PARARNN_STATUS_TIMEOUT where a wait between the
+ * CTAs of a cluster ran out; the states that depend on what was waited for are
+ * then NaN (without a status word too).  opts (NULL: the defaults):
+ * timeout_us bounds each wait (0: 2 s); with PARARNN_FLAG_INJECT_WITHHOLD, for
+ * testing, the CTA of cluster rank inject_chunk % 8 sends no map from the
+ * cluster's round inject_chunk / 8 on (counted in the order of the scan), so
+ * that the waits for it run out.  Other fields are ignored. */
+int pararnn_linrec_solve_ex(int cell, const void* u, int u_dtype,
+                            long long u_stride_b, long long u_stride_t,
+                            long long u_stride_g, const float* lam,
+                            const float* bias, const float* h0,
+                            const unsigned char* reset, float* h, int B, int T,
+                            int D, float kappa, int* status,
+                            const pararnn_opts* opts, pararnn_stream_t stream);
+
 /* Bytes of workspace pararnn_linrec_adjoint needs (0 on invalid sizes).  It
  * needs no initialisation and keeps nothing from call to call; calls that
  * overlap on the GPU need one each. */
@@ -533,6 +549,20 @@ int pararnn_linrec_adjoint(int cell, const void* u, int u_dtype,
                            float* dlam, float* dbias, float* dh0, int B,
                            int T, int D, float kappa, void* workspace,
                            size_t ws_bytes, pararnn_stream_t stream);
+
+/* pararnn_linrec_adjoint with options and a status word, as for the solve
+ * (gradients in place of states). */
+int pararnn_linrec_adjoint_ex(int cell, const void* u, int u_dtype,
+                              long long u_stride_b, long long u_stride_t,
+                              long long u_stride_g, const float* lam,
+                              const float* bias, const float* h0,
+                              const unsigned char* reset, const float* h,
+                              const float* dLdh, void* du, int du_dtype,
+                              float* dlam, float* dbias, float* dh0, int B,
+                              int T, int D, float kappa, int* status,
+                              void* workspace, size_t ws_bytes,
+                              const pararnn_opts* opts,
+                              pararnn_stream_t stream);
 
 /* One decode step: u_t (b, q, d) at u_t[b * u_stride_b + q * u_stride_g + d],
  * h_prev [B][D] or NULL (zeros), h_next [B][D] (may be h_prev). */

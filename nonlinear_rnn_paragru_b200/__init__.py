@@ -35,7 +35,8 @@ __all__ = [
     "gru_step", "lstm_step",
     "PARARNN_LIN_GRU", "PARARNN_LIN_DECAY", "PARARNN_ACT_SILU", "PARARNN_ACT_SIGMOID",
     "pararnn_linrec_solve", "pararnn_linrec_workspace_size", "pararnn_linrec_adjoint",
-    "pararnn_linrec_step", "linrec_solve", "linrec_adjoint", "linrec_step",
+    "pararnn_linrec_solve_ex", "pararnn_linrec_adjoint_ex", "pararnn_linrec_step", "linrec_solve",
+    "linrec_adjoint", "linrec_step",
     "pararnn_block_norm", "pararnn_block_norm_workspace_size", "pararnn_block_norm_adjoint",
     "block_norm", "block_norm_adjoint",
     "Workspace", "read_stats",
@@ -119,9 +120,13 @@ def load_library():
         "pararnn_gru_step": (i, [vp, i, fp, fp, fp, fp, i, i, vp]),
         "pararnn_lstm_step": (i, [vp, i, fp, fp, fp, fp, fp, fp, i, i, vp]),
         "pararnn_linrec_solve": (i, [i, vp, i, ll, ll, ll, fp, fp, fp, vp, fp, i, i, i, fl, vp]),
+        "pararnn_linrec_solve_ex": (i, [i, vp, i, ll, ll, ll, fp, fp, fp, vp, fp, i, i, i, fl, ip, op,
+                                        vp]),
         "pararnn_linrec_workspace_size": (sz, [i, i, i, i]),
         "pararnn_linrec_adjoint": (i, [i, vp, i, ll, ll, ll, fp, fp, fp, vp, fp, fp, vp, i, fp, fp,
                                        fp, i, i, i, fl, vp, sz, vp]),
+        "pararnn_linrec_adjoint_ex": (i, [i, vp, i, ll, ll, ll, fp, fp, fp, vp, fp, fp, vp, i, fp, fp,
+                                          fp, i, i, i, fl, ip, vp, sz, op, vp]),
         "pararnn_linrec_step": (i, [i, vp, i, ll, ll, fp, fp, fp, fp, i, i, fl, vp]),
         "pararnn_block_norm": (i, [vp, i, ll, vp, i, ll, i, fp, vp, i, ll, fp, fp, vp, i, vp, i, fl,
                                    ll, i, vp]),
@@ -602,6 +607,15 @@ def pararnn_linrec_solve(cell, u, lam, bias, h0, reset, h, kappa=8.0, stream=Non
         _ptr(reset, None), _ptr(h), B, T, D, kappa, _stream(stream)), "pararnn_linrec_solve")
 
 
+def pararnn_linrec_solve_ex(cell, u, lam, bias, h0, reset, h, status, opts, kappa=8.0, stream=None):
+    B, T, G, D = u.shape
+    _check(load_library().pararnn_linrec_solve_ex(
+        cell, u.data_ptr(), _code(u), *_lin_u(cell, u, 4)[2], _ptr(lam), _ptr(bias), _ptr(h0),
+        _ptr(reset, None), _ptr(h), B, T, D, kappa, _iptr(status),
+        ctypes.byref(opts) if opts is not None else None, _stream(stream)),
+        "pararnn_linrec_solve_ex")
+
+
 def pararnn_linrec_workspace_size(cell, B, T, D) -> int:
     return int(load_library().pararnn_linrec_workspace_size(cell, B, T, D))
 
@@ -617,6 +631,18 @@ def pararnn_linrec_adjoint(cell, u, lam, bias, h0, reset, h, dLdh, du, dlam, dbi
         "pararnn_linrec_adjoint")
 
 
+def pararnn_linrec_adjoint_ex(cell, u, lam, bias, h0, reset, h, dLdh, du, dlam, dbias, dh0, status,
+                              workspace, opts, kappa=8.0, stream=None):
+    B, T, G, D = u.shape
+    _check(load_library().pararnn_linrec_adjoint_ex(
+        cell, u.data_ptr(), _code(u), *_lin_u(cell, u, 4)[2], _ptr(lam), _ptr(bias), _ptr(h0),
+        _ptr(reset, None), _ptr(h), _ptr(dLdh), _ptr(du, None), _code(du), _ptr(dlam),
+        _ptr(dbias), _ptr(dh0), B, T, D, kappa, _iptr(status), _wptr(workspace),
+        workspace.numel() * workspace.element_size(),
+        ctypes.byref(opts) if opts is not None else None, _stream(stream)),
+        "pararnn_linrec_adjoint_ex")
+
+
 def pararnn_linrec_step(cell, u_t, lam, bias, h_prev, h_next, kappa=8.0, stream=None):
     B, G, D = u_t.shape
     _check(load_library().pararnn_linrec_step(
@@ -624,35 +650,45 @@ def pararnn_linrec_step(cell, u_t, lam, bias, h_prev, h_next, kappa=8.0, stream=
         _ptr(h_prev), _ptr(h_next), B, D, kappa, _stream(stream)), "pararnn_linrec_step")
 
 
+def _wait_args(status, opts, dev):
+    """Pointers of a call's status word (int32 [1]) and its options."""
+    return (_need(status, "status", (1,), dev, (torch.int32,)),
+            None if opts is None else ctypes.byref(opts))
+
+
 def linrec_solve(cell, u, lam=None, bias=None, h0=None, *, reset=None, kappa=8.0, out=None,
-                 stream=None):
+                 status=None, opts=None, stream=None):
     """Gated linear recurrence: u [B, T, G, D] (bf16 or fp32) -> states h
     [B, T, D] fp32.  cell PARARNN_LIN_GRU (G = 2: z, c) or PARARNN_LIN_DECAY
     (G = 3: r, i, x, with lam [D]).  u may be a view into a larger projection
     (channels contiguous, strides multiples of 8 elements, 16-byte aligned).
     reset [B, T] (bool or uint8): the state that enters a marked step is zero.
-    `out`: the tensor to write h to."""
+    `out`: the tensor to write h to.  `status`: an int32 [1] CUDA tensor that
+    receives 0, or the TIMEOUT status where a wait inside the kernel ran out
+    (what depends on it is NaN); `opts` bounds those waits (timeout_us)."""
     dev, G, st = _lin_u(cell, u, 4)
     B, T, _, D = u.shape
     lp, bp, hp = _lin_params(cell, dev, B, G, D, lam, bias, h0)
     rp = _need(reset, "reset", (B, T), dev, _MASKS)
+    wait = _wait_args(status, opts, dev)
     op = _need(out, "out", (B, T, D), dev)
     with _on(dev, stream):
         if out is None:
             out = u.new_empty((B, T, D), dtype=_F32)
             op = out.data_ptr()
-        _check(load_library().pararnn_linrec_solve(
-            cell, u.data_ptr(), _code(u), *st, lp, bp, hp, rp, op, B, T, D, kappa,
+        _check(load_library().pararnn_linrec_solve_ex(
+            cell, u.data_ptr(), _code(u), *st, lp, bp, hp, rp, op, B, T, D, kappa, *wait,
             _raw_stream(dev.index)), "pararnn_linrec_solve")
     return out
 
 
 def linrec_adjoint(cell, u, lam, bias, h0, h, dLdh, *, reset=None, kappa=8.0, want_params=True,
-                   want_dh0=True, du_dtype=None, out=None, stream=None):
+                   want_dh0=True, du_dtype=None, out=None, status=None, opts=None, stream=None):
     """Adjoint of :func:`linrec_solve` along its states h: a dict of du
     [B, T, G, D] (u's type, or `du_dtype` = torch.float32), dlam [D], dbias
     [G, D] and dh0 [B, D] (None where not wanted or absent).  `out`: a dict of
-    tensors to write to instead of new ones."""
+    tensors to write to instead of new ones.  `status`, `opts`: as for
+    linrec_solve."""
     dev, G, st = _lin_u(cell, u, 4)
     B, T, _, D = u.shape
     lp, bp, hp = _lin_params(cell, dev, B, G, D, lam, bias, h0)
@@ -667,6 +703,7 @@ def linrec_adjoint(cell, u, lam, bias, h0, h, dLdh, *, reset=None, kappa=8.0, wa
         _need(dlam, "dlam", (D,), dev)
         _need(dbias, "dbias", (G, D), dev)
         _need(dh0, "dh0", (B, D), dev)
+    sw, ow = _wait_args(status, opts, dev)
     lib = load_library()
     with _on(dev, stream):
         if du is None:
@@ -686,10 +723,10 @@ def linrec_adjoint(cell, u, lam, bias, h0, h, dLdh, *, reset=None, kappa=8.0, wa
             dh0 = _like(h0, (B, D), _F32, u)
         nbytes = max(256, lib.pararnn_linrec_workspace_size(cell, B, T, D))
         ws = u.new_empty(nbytes, dtype=torch.uint8)
-        _check(lib.pararnn_linrec_adjoint(
+        _check(lib.pararnn_linrec_adjoint_ex(
             cell, u.data_ptr(), _code(u), *st, lp, bp, hp, rp, sp, gp, du.data_ptr(), _code(du),
-            _any_ptr(dlam), _any_ptr(dbias), _any_ptr(dh0), B, T, D, kappa, ws.data_ptr(), nbytes,
-            _raw_stream(dev.index)), "pararnn_linrec_adjoint")
+            _any_ptr(dlam), _any_ptr(dbias), _any_ptr(dh0), B, T, D, kappa, sw, ws.data_ptr(),
+            nbytes, ow, _raw_stream(dev.index)), "pararnn_linrec_adjoint")
     return {"du": du, "dlam": dlam, "dbias": dbias, "dh0": dh0}
 
 

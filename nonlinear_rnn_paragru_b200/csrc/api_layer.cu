@@ -24,6 +24,19 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 
 bool is_dtype(int t) { return t == PARARNN_F32 || t == PARARNN_BF16; }
 
+constexpr unsigned long long kWaitNs = 2000000000ull;  // bound on a wait without opts
+
+// what the opts of an _ex call say of its waits
+void wait_opts(const pararnn_opts* opts, unsigned long long& wait_ns, int& withhold) {
+  wait_ns = opts && opts->timeout_us ? 1000ull * opts->timeout_us : kWaitNs;
+  withhold = opts && (opts->flags & PARARNN_FLAG_INJECT_WITHHOLD) ? opts->inject_chunk : -1;
+}
+
+// the status word starts at 0; kernels write it where a wait runs out
+bool clear_status(int* status, cudaStream_t stream) {
+  return !status || cudaMemsetAsync(status, 0, sizeof(int), stream) == cudaSuccess;
+}
+
 bool stride_ok(long long s) { return s >= 0 && s % 8 == 0; }
 
 // what the three recurrence calls check alike; T = 1 for the step
@@ -43,6 +56,8 @@ int lin_args(int cell, const void* u, int u_dtype, long long sb, long long st, l
 LinParams lin_params(const void* u, long long sb, long long st, long long sg, const float* lam, const float* bias,
                      const float* h0, const unsigned char* reset, int B, int T, int D, float kappa) {
   LinParams p = {};
+  p.wait_ns = kWaitNs;
+  p.withhold = -1;
   p.u = u;
   p.sb = sb;
   p.st = st;
@@ -104,13 +119,24 @@ int pararnn_linrec_solve(int cell, const void* u, int u_dtype, long long u_strid
                          long long u_stride_g, const float* lam, const float* bias, const float* h0,
                          const unsigned char* reset, float* h, int B, int T, int D, float kappa,
                          pararnn_stream_t stream) {
+  return pararnn_linrec_solve_ex(cell, u, u_dtype, u_stride_b, u_stride_t, u_stride_g, lam, bias, h0, reset, h, B, T,
+                                 D, kappa, nullptr, nullptr, stream);
+}
+
+int pararnn_linrec_solve_ex(int cell, const void* u, int u_dtype, long long u_stride_b, long long u_stride_t,
+                            long long u_stride_g, const float* lam, const float* bias, const float* h0,
+                            const unsigned char* reset, float* h, int B, int T, int D, float kappa, int* status,
+                            const pararnn_opts* opts, pararnn_stream_t stream) {
   const int rc = lin_args(cell, u, u_dtype, u_stride_b, u_stride_t, u_stride_g, lam, bias, B, T, D, kappa);
   if (rc) return rc;
   if (!h) return PARARNN_ERR_INVALID_ARG;
   if (linrec_most_ctas(B, D) >= (1LL << 31)) return PARARNN_ERR_TOO_LARGE;
-  if (!aligned(h, 16) || (h0 && !aligned(h0, 4))) return PARARNN_ERR_MISALIGNED;
+  if (!aligned(h, 16) || (h0 && !aligned(h0, 4)) || (status && !aligned(status, 4))) return PARARNN_ERR_MISALIGNED;
   LinParams p = lin_params(u, u_stride_b, u_stride_t, u_stride_g, lam, bias, h0, reset, B, T, D, kappa);
   p.h = h;
+  p.status = status;
+  wait_opts(opts, p.wait_ns, p.withhold);
+  if (!clear_status(status, (cudaStream_t)stream)) return PARARNN_ERR_CUDA;
   return done(launch_linrec_fwd(cell, u_dtype == PARARNN_BF16, p, (cudaStream_t)stream));
 }
 
@@ -125,6 +151,17 @@ int pararnn_linrec_adjoint(int cell, const void* u, int u_dtype, long long u_str
                            const unsigned char* reset, const float* h, const float* dLdh, void* du,
                            int du_dtype, float* dlam, float* dbias, float* dh0, int B, int T, int D,
                            float kappa, void* workspace, size_t ws_bytes, pararnn_stream_t stream) {
+  return pararnn_linrec_adjoint_ex(cell, u, u_dtype, u_stride_b, u_stride_t, u_stride_g, lam, bias, h0, reset, h,
+                                   dLdh, du, du_dtype, dlam, dbias, dh0, B, T, D, kappa, nullptr, workspace, ws_bytes,
+                                   nullptr, stream);
+}
+
+int pararnn_linrec_adjoint_ex(int cell, const void* u, int u_dtype, long long u_stride_b, long long u_stride_t,
+                              long long u_stride_g, const float* lam, const float* bias, const float* h0,
+                              const unsigned char* reset, const float* h, const float* dLdh, void* du,
+                              int du_dtype, float* dlam, float* dbias, float* dh0, int B, int T, int D,
+                              float kappa, int* status, void* workspace, size_t ws_bytes,
+                              const pararnn_opts* opts, pararnn_stream_t stream) {
   const int rc = lin_args(cell, u, u_dtype, u_stride_b, u_stride_t, u_stride_g, lam, bias, B, T, D, kappa);
   if (rc) return rc;
   if (!h || !dLdh || !du || !workspace || (cell == PARARNN_LIN_GRU && dlam)) return PARARNN_ERR_INVALID_ARG;
@@ -133,7 +170,7 @@ int pararnn_linrec_adjoint(int cell, const void* u, int u_dtype, long long u_str
   if (linrec_most_ctas(B, D) >= (1LL << 31)) return PARARNN_ERR_TOO_LARGE;
   if (!aligned(h, 16) || !aligned(dLdh, 16) || !aligned(du, 16) || (h0 && !aligned(h0, 4)) ||
       (dlam && !aligned(dlam, 4)) || (dbias && !aligned(dbias, 4)) || (dh0 && !aligned(dh0, 4)) ||
-      !aligned(workspace, 256))
+      (status && !aligned(status, 4)) || !aligned(workspace, 256))
     return PARARNN_ERR_MISALIGNED;
   if (ws_bytes < pararnn_linrec_workspace_size(cell, B, T, D)) return PARARNN_ERR_WORKSPACE_TOO_SMALL;
   LinParams p = lin_params(u, u_stride_b, u_stride_t, u_stride_g, lam, bias, h0, reset, B, T, D, kappa);
@@ -142,6 +179,9 @@ int pararnn_linrec_adjoint(int cell, const void* u, int u_dtype, long long u_str
   p.du = du;
   p.dh0 = dh0;
   p.part = static_cast<float*>(workspace);
+  p.status = status;
+  wait_opts(opts, p.wait_ns, p.withhold);
+  if (!clear_status(status, (cudaStream_t)stream)) return PARARNN_ERR_CUDA;
   return done(launch_linrec_bwd(cell, u_dtype == PARARNN_BF16, du_dtype == PARARNN_BF16, p, dlam, dbias,
                                 (cudaStream_t)stream));
 }

@@ -88,8 +88,6 @@ __device__ __forceinline__ void st_async16(uint32_t addr, uint32_t bar, float4 v
       : "memory");
 }
 
-constexpr uint64_t kLinWaitNs = 2000000000ull;
-
 template <int CL, int GL, bool kReset>
 __device__ __forceinline__ float2 lin_join(const float4* cta, int rpos, int gl, float2& carry) {
   float4 v[CL];
@@ -110,13 +108,14 @@ struct LinTurn {
   float4 before, all;
 };
 
-// Publish the thread's map of round r, and the CTA's to the cluster.  Positions
-// (gpos of the group in the CTA, rpos of the CTA) run in the order of the scan.
-// The groups' buffers alternate: round r + 2's are written after the barrier of
-// round r + 1, which each warp reaches after it read round r's.
+// Publish the thread's map of round r, and (with `send`) the CTA's to the
+// cluster.  Positions (gpos of the group in the CTA, rpos of the CTA) run in the
+// order of the scan.  The groups' buffers alternate: round r + 2's are written
+// after the barrier of round r + 1, which each warp reaches after it read round
+// r's.
 template <int W, int GL, bool kReset>
 __device__ __forceinline__ LinTurn lin_publish(LinShared<W>& sh, float4* cta, unsigned r, float4 mine, int rpos,
-                                               int CL) {
+                                               int CL, bool send) {
   constexpr int NP = W * 32 / GL;
   const int gl = threadIdx.x % GL, gpos = threadIdx.x / GL;
   sh.map[r & 1][threadIdx.x] = mine;
@@ -131,7 +130,7 @@ __device__ __forceinline__ LinTurn lin_publish(LinShared<W>& sh, float4* cta, un
     if (i < gpos) t.before = i ? lin_then<kReset>(t.before, v) : v;
     if (i && CL == 1) t.all = lin_then<kReset>(t.all, v);
   }
-  if (CL > 1 && gpos == NP - 1) {
+  if (CL > 1 && gpos == NP - 1 && send) {
     const float4 all = lin_then<kReset>(t.before, mine);
     const int buf = r % kLinBufs;
     if (gl == 0) mbar_arrive_expect_tx(&sh.bar[buf], CL * GL * 16);
@@ -147,17 +146,19 @@ __device__ __forceinline__ LinTurn lin_publish(LinShared<W>& sh, float4* cta, un
 // sends round r + 4's map after it ended round r + 2, for which it had every
 // CTA's map of that round, each sent after all its warps had ended round r
 // (rounds are published at most one ahead of their end).  The wait is bounded;
-// where it runs out the states become NaN.
+// a thread whose wait runs out is lost (stop = 0): it carries NaN from there on,
+// waits no more and sends no more, so that no buffer or mbarrier is used out of
+// turn (the CTAs that miss its maps run out of time in turn, once each).
 template <int W, int GL, bool kReset>
 __device__ __forceinline__ float2 lin_enter(LinShared<W>& sh, const float4* cta, unsigned r, const LinTurn& t,
-                                            int rpos, int CL, float2& carry, bool& lost) {
+                                            int rpos, int CL, float2& carry, unsigned& stop, uint64_t wait_ns) {
   const int gl = threadIdx.x % GL, gpos = threadIdx.x / GL;
   float2 in = carry;
   if (CL == 1) {
     carry = lin_apply<kReset>(t.all, carry);
   } else {
     const int buf = r % kLinBufs;
-    if (!lost) lost = !mbar_wait_bounded(&sh.bar[buf], (r / kLinBufs) & 1, kLinWaitNs);
+    if (stop && !mbar_wait_bounded(&sh.bar[buf], (r / kLinBufs) & 1, wait_ns)) stop = 0;
     const float4* v = cta + buf * CL * GL;
     if (CL == 2)
       in = lin_join<2, GL, kReset>(v, rpos, gl, carry);
@@ -165,9 +166,15 @@ __device__ __forceinline__ float2 lin_enter(LinShared<W>& sh, const float4* cta,
       in = lin_join<4, GL, kReset>(v, rpos, gl, carry);
     else
       in = lin_join<8, GL, kReset>(v, rpos, gl, carry);
-    if (lost) carry = in = both(__int_as_float(0x7fffffff));
+    if (!stop) carry = in = both(__int_as_float(0x7fffffff));
   }
   return gpos ? lin_apply<kReset>(t.before, in) : in;
+}
+
+// The round from which on this thread sends no map (see LinParams): none, and 0
+// once it is lost.
+__device__ __forceinline__ unsigned lin_stop(const LinParams& p, int rank, int CL) {
+  return CL > 1 && p.withhold >= 0 && (p.withhold & 7) == rank ? p.withhold / 8 : 0xffffffffu;
 }
 
 // Before the rounds: the mbarriers, and every CTA of the cluster runs before
@@ -178,6 +185,18 @@ __device__ __forceinline__ void lin_cluster_start(LinShared<W>& sh, int CL) {
   if (threadIdx.x == 0)
     for (int i = 0; i < kLinBufs; ++i) mbar_init(&sh.bar[i], 1);
   cg::this_cluster().sync();
+}
+
+// The last thing a thread does.  A CTA's shared memory must outlive the stores
+// of its peers: one whose waits ended has them all; a lost thread waits until
+// every thread of the cluster is lost too or has left (all waits are bounded),
+// and then for the stores on their way, which take microseconds.
+__device__ __forceinline__ void lin_leave(unsigned stop, int* status) {
+  if (stop) return;
+  if (status) *status = PARARNN_STATUS_TIMEOUT;
+  asm volatile("barrier.cluster.arrive;\n barrier.cluster.wait;" ::: "memory");
+  const uint64_t t0 = globaltimer_ns();
+  while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
 }
 
 // A group's marks: its j-th step in the order of the scan has its mark at
@@ -308,7 +327,7 @@ __global__ void __launch_bounds__(32 * FwdShape<CELL, kBF16, V>::W, FwdShape<CEL
   const size_t row = (size_t)b * p.T;
   lin_cluster_start(sh, CL);
   const int rounds = (p.T + round - 1) / round;
-  bool lost = false;
+  unsigned stop = lin_stop(p, rank, CL);
   int slot = 0;
   struct Round {
     float2 P[K], Q[K];  // h after step j is P[j] h_in + Q[j]
@@ -347,11 +366,11 @@ __global__ void __launch_bounds__(32 * FwdShape<CELL, kBF16, V>::W, FwdShape<CEL
     by_marks<kReset>(x.resets, compose);
     float4 map = make_float4(x.P[K - 1].x, x.P[K - 1].y, x.Q[K - 1].x, x.Q[K - 1].y);
     if (kReset && x.resets) map.x = map.y = -1.f;
-    x.turn = lin_publish<W, GL, kReset>(sh, cta, r, map, rank, CL);
+    x.turn = lin_publish<W, GL, kReset>(sh, cta, r, map, rank, CL, (unsigned)r < stop);
   };
   auto end = [&](int r, Round& x) {  // its states, stored
     const int t0 = r * round + first + grp * K;
-    const float2 in = lin_enter<W, GL, kReset>(sh, cta, r, x.turn, rank, CL, carry, lost);
+    const float2 in = lin_enter<W, GL, kReset>(sh, cta, r, x.turn, rank, CL, carry, stop, p.wait_ns);
 #pragma unroll
     for (int j = 0; j < K; ++j) {
       const float2 h = lfma(x.P[j], in, x.Q[j]);
@@ -386,6 +405,7 @@ __global__ void __launch_bounds__(32 * FwdShape<CELL, kBF16, V>::W, FwdShape<CEL
     }
   }
   cp_async_wait<0>();
+  lin_leave(stop, p.status);
 }
 
 // Reverse scan: lambda_t = g_t + mu_{t+1}, mu_t = (1 - m_t) lambda_t (0 at a
@@ -473,7 +493,7 @@ __global__ void __launch_bounds__(32 * BwdShape<CELL, kBF16, V>::W, BwdShape<CEL
 #pragma unroll
   for (int q = 0; q <= G; ++q) sum[q] = both(0.f);
   lin_cluster_start(sh, CL);
-  bool lost = false;
+  unsigned stop = lin_stop(p, rank, CL);
   int slot = 0;
   unsigned nround = 0;
   using Out = typename std::conditional<kBF16Out, __nv_bfloat162, float2>::type;
@@ -512,8 +532,9 @@ __global__ void __launch_bounds__(32 * BwdShape<CELL, kBF16, V>::W, BwdShape<CEL
     by_marks<kReset>(resets, compose);
     if (kReset && resets) pr = both(-1.f);
     const LinTurn turn =
-        lin_publish<W, GL, kReset>(sh, cta, nround, make_float4(pr.x, pr.y, mu.x, mu.y), rank, CL);
-    mu = lin_enter<W, GL, kReset>(sh, cta, nround, turn, rank, CL, carry, lost);
+        lin_publish<W, GL, kReset>(sh, cta, nround, make_float4(pr.x, pr.y, mu.x, mu.y), rank, CL,
+                                   nround < stop);
+    mu = lin_enter<W, GL, kReset>(sh, cta, nround, turn, rank, CL, carry, stop, p.wait_ns);
     float2 add[G + 1];
 #pragma unroll
     for (int q = 0; q <= G; ++q) add[q] = both(0.f);
@@ -563,24 +584,26 @@ __global__ void __launch_bounds__(32 * BwdShape<CELL, kBF16, V>::W, BwdShape<CEL
     for (int q = 0; q <= G; ++q) sum[q] = ladd(sum[q], add[q]);
   }
   cp_async_wait<0>();
-  if (!p.part) return;
-  if (CELL == PARARNN_LIN_DECAY) sum[G] = lmul(sum[G], Cell::lam_scale(p.lam, d));
-  // the groups' sums, in their order
-  constexpr int NS = CELL == PARARNN_LIN_DECAY ? G + 1 : G;
-  __syncthreads();
-  float2* const acc = reinterpret_cast<float2*>(ring);  // [NS][W * 32]
-  static_assert(Shape::kBytes >= W * NS * 32 * (int)sizeof(float2), "sums fit");
-  static_assert(W >= NS, "a warp for each sum");
+  if (p.part) {
+    if (CELL == PARARNN_LIN_DECAY) sum[G] = lmul(sum[G], Cell::lam_scale(p.lam, d));
+    // the groups' sums, in their order
+    constexpr int NS = CELL == PARARNN_LIN_DECAY ? G + 1 : G;
+    __syncthreads();
+    float2* const acc = reinterpret_cast<float2*>(ring);  // [NS][W * 32]
+    static_assert(Shape::kBytes >= W * NS * 32 * (int)sizeof(float2), "sums fit");
+    static_assert(W >= NS, "a warp for each sum");
 #pragma unroll
-  for (int q = 0; q < NS; ++q) acc[q * W * 32 + threadIdx.x] = sum[q];
-  __syncthreads();
-  if (warp < NS && lane < GL && live) {
-    float2 s = both(0.f);
-    for (int i = 0; i < W * 32 / GL; ++i) s = ladd(s, acc[warp * W * 32 + i * GL + lane]);
-    float* q = p.part + ((size_t)(b * CL + rank) * NS + warp) * p.D + d;
-    q[0] = s.x;
-    q[1] = s.y;
+    for (int q = 0; q < NS; ++q) acc[q * W * 32 + threadIdx.x] = sum[q];
+    __syncthreads();
+    if (warp < NS && lane < GL && live) {
+      float2 s = both(0.f);
+      for (int i = 0; i < W * 32 / GL; ++i) s = ladd(s, acc[warp * W * 32 + i * GL + lane]);
+      float* q = p.part + ((size_t)(b * CL + rank) * NS + warp) * p.D + d;
+      q[0] = s.x;
+      q[1] = s.y;
+    }
   }
+  lin_leave(stop, p.status);
 }
 
 // One decode step: a thread owns two channels of one row; h_prev may be h_next.

@@ -236,6 +236,9 @@ struct LinParams {
   float* part;           // adjoint: [B * CL][G or, with dlam, G + 1][D] sums over a CTA's steps
   int B, T, D;
   int ntd;               // tiles of a batch row (set at the launch)
+  int* status;           // device word for a wait that ran out, or NULL
+  unsigned long long wait_ns;  // bound on a wait for the cluster's maps
+  int withhold;          // testing: 8 round + rank that sends no map from that round on; -1: none
 };
 
 }  // namespace pararnn

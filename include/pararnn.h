@@ -620,6 +620,24 @@ int pararnn_block_norm_adjoint(
     long long N, int D, void* workspace, size_t ws_bytes,
     pararnn_stream_t stream);
 
+/* pararnn_block_norm_adjoint with options and a status word.  *status (device
+ * int, NULL to skip) receives 0, or PARARNN_STATUS_TIMEOUT where a wait for a
+ * row's copies into shared memory ran out; the gradients that depend on what
+ * was waited for are then NaN (without a status word too).  opts (NULL: the
+ * defaults): timeout_us bounds each wait (0: 2 s); with
+ * PARARNN_FLAG_INJECT_WITHHOLD, for testing, row inject_chunk is not copied
+ * (D > 256; narrower rows are copied by the threads that use them).  Other
+ * fields are ignored. */
+int pararnn_block_norm_adjoint_ex(
+    const void* h, int h_dtype, long long h_stride, const void* gate,
+    int gate_dtype, long long gate_stride, int act, const float* w_post,
+    const void* res, int res_dtype, long long res_stride, const float* scale,
+    const float* w_pre, const void* ds, int ds_dtype, long long ds_stride,
+    const void* dx, int dx_dtype, long long dx_stride, void* dh, void* dgate,
+    void* dres, float* dw_post, float* dscale, float* dw_pre, float eps,
+    long long N, int D, int* status, void* workspace, size_t ws_bytes,
+    const pararnn_opts* opts, pararnn_stream_t stream);
+
 /* Human-readable text for a return code. */
 const char* pararnn_strerror(int code);
 

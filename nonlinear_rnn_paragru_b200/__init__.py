@@ -38,7 +38,7 @@ __all__ = [
     "pararnn_linrec_solve_ex", "pararnn_linrec_adjoint_ex", "pararnn_linrec_step", "linrec_solve",
     "linrec_adjoint", "linrec_step",
     "pararnn_block_norm", "pararnn_block_norm_workspace_size", "pararnn_block_norm_adjoint",
-    "block_norm", "block_norm_adjoint",
+    "pararnn_block_norm_adjoint_ex", "block_norm", "block_norm_adjoint",
     "Workspace", "read_stats",
 ]
 
@@ -133,6 +133,9 @@ def load_library():
         "pararnn_block_norm_workspace_size": (sz, [ll, i]),
         "pararnn_block_norm_adjoint": (i, [vp, i, ll, vp, i, ll, i, fp, vp, i, ll, fp, fp, vp, i, ll,
                                            vp, i, ll, vp, vp, vp, fp, fp, fp, fl, ll, i, vp, sz, vp]),
+        "pararnn_block_norm_adjoint_ex": (i, [vp, i, ll, vp, i, ll, i, fp, vp, i, ll, fp, fp, vp, i, ll,
+                                              vp, i, ll, vp, vp, vp, fp, fp, fp, fl, ll, i, ip, vp, sz,
+                                              op, vp]),
         "pararnn_strerror": (ctypes.c_char_p, [i]),
     }
     for name, (res, args) in sigs.items():
@@ -775,6 +778,19 @@ def pararnn_block_norm_adjoint(h, h_stride, gate, gate_stride, act, w_post, res,
         "pararnn_block_norm_adjoint")
 
 
+def pararnn_block_norm_adjoint_ex(h, h_stride, gate, gate_stride, act, w_post, res, res_stride, scale,
+                                  w_pre, ds, ds_stride, dx, dx_stride, dh, dgate, dres, dw_post, dscale,
+                                  dw_pre, eps, N, D, status, workspace, opts, stream=None):
+    _check(load_library().pararnn_block_norm_adjoint_ex(
+        h.data_ptr(), _code(h), h_stride, _any_ptr(gate), _code(gate), gate_stride, act, _ptr(w_post),
+        _any_ptr(res), _code(res), res_stride, _ptr(scale), _ptr(w_pre), _any_ptr(ds), _code(ds),
+        ds_stride, _any_ptr(dx), _code(dx), dx_stride, _ptr(dh, None), _ptr(dgate, None),
+        _ptr(dres, None), _ptr(dw_post), _ptr(dscale), _ptr(dw_pre), eps, N, D, _iptr(status),
+        _wptr(workspace), workspace.numel() * workspace.element_size(),
+        ctypes.byref(opts) if opts is not None else None, _stream(stream)),
+        "pararnn_block_norm_adjoint_ex")
+
+
 def _rows(t, name, shape, dev):
     """(pointer, type code, row stride in elements) of a [..., D] tensor whose
     leading axes make up one axis of rows (None -> NULL)."""
@@ -846,16 +862,17 @@ def block_norm(h, *, gate=None, act="silu", w_post=None, res=None, scale=None, w
 
 
 def block_norm_adjoint(h, ds, dx, *, gate=None, act="silu", w_post=None, res=None, scale=None,
-                       w_pre=None, eps=1e-6, stream=None):
+                       w_pre=None, eps=1e-6, status=None, opts=None, stream=None):
     """Adjoint of :func:`block_norm` from ds = dL/ds (or None) and dx = dL/dx
     (given exactly when w_pre is): a dict of dh, dgate, dres (contiguous, in
     the types of h, gate, res) and dw_post, dscale, dw_pre [D] fp32, None
     where the part is absent.  h, gate and res hold what the forward call
-    read."""
+    read.  `status`, `opts`: as for linrec_solve."""
     dev, shape, N, D, parts = _norm_parts(h, gate, act, w_post, res, scale, w_pre)
     if (dx is None) != (w_pre is None):
         raise ValueError("dx: given exactly when w_pre is")
     given = (*_rows(ds, "ds", shape, dev), *_rows(dx, "dx", shape, dev))
+    sw, ow = _wait_args(status, opts, dev)
     with _on(dev, stream):
         def like(t):
             return None if t is None else _like(t, shape, t.dtype, t)
@@ -864,7 +881,7 @@ def block_norm_adjoint(h, ds, dx, *, gate=None, act="silu", w_post=None, res=Non
         lib = load_library()
         nbytes = max(256, lib.pararnn_block_norm_workspace_size(N, D))
         ws = h.new_empty(nbytes, dtype=torch.uint8)
-        _check(lib.pararnn_block_norm_adjoint(*parts, *given, *map(_any_ptr, outs), eps, N, D,
-                                              ws.data_ptr(), nbytes, _raw_stream(dev.index)),
+        _check(lib.pararnn_block_norm_adjoint_ex(*parts, *given, *map(_any_ptr, outs), eps, N, D, sw,
+                                                 ws.data_ptr(), nbytes, ow, _raw_stream(dev.index)),
                "pararnn_block_norm_adjoint")
     return dict(zip(("dh", "dgate", "dres", "dw_post", "dscale", "dw_pre"), outs))

@@ -229,6 +229,20 @@ int pararnn_block_norm_adjoint(const void* h, int h_dtype, long long h_stride, c
                                long long dx_stride, void* dh, void* dgate, void* dres, float* dw_post,
                                float* dscale, float* dw_pre, float eps, long long N, int D, void* workspace,
                                size_t ws_bytes, pararnn_stream_t stream) {
+  return pararnn_block_norm_adjoint_ex(h, h_dtype, h_stride, gate, gate_dtype, gate_stride, act, w_post, res, res_dtype,
+                                       res_stride, scale, w_pre, ds, ds_dtype, ds_stride, dx, dx_dtype, dx_stride, dh,
+                                       dgate, dres, dw_post, dscale, dw_pre, eps, N, D, nullptr, workspace, ws_bytes,
+                                       nullptr, stream);
+}
+
+int pararnn_block_norm_adjoint_ex(const void* h, int h_dtype, long long h_stride, const void* gate, int gate_dtype,
+                                  long long gate_stride, int act, const float* w_post, const void* res,
+                                  int res_dtype, long long res_stride, const float* scale, const float* w_pre,
+                                  const void* ds, int ds_dtype, long long ds_stride, const void* dx, int dx_dtype,
+                                  long long dx_stride, void* dh, void* dgate, void* dres, float* dw_post,
+                                  float* dscale, float* dw_pre, float eps, long long N, int D, int* status,
+                                  void* workspace, size_t ws_bytes, const pararnn_opts* opts,
+                                  pararnn_stream_t stream) {
   const int rc = norm_args(h, h_dtype, h_stride, gate, gate_dtype, gate_stride, act, w_post, res, res_dtype,
                            res_stride, scale, w_pre, eps, N, D);
   if (rc) return rc;
@@ -241,7 +255,7 @@ int pararnn_block_norm_adjoint(const void* h, int h_dtype, long long h_stride, c
   for (const void* q : {ds, dx, (const void*)dh, (const void*)dgate, (const void*)dres, (const void*)dw_post,
                         (const void*)dscale, (const void*)dw_pre})
     if (!aligned(q, 16)) return PARARNN_ERR_MISALIGNED;
-  if (!aligned(workspace, 256)) return PARARNN_ERR_MISALIGNED;
+  if (!aligned(workspace, 256) || (status && !aligned(status, 4))) return PARARNN_ERR_MISALIGNED;
   if (ws_bytes < pararnn_block_norm_workspace_size(N, D)) return PARARNN_ERR_WORKSPACE_TOO_SMALL;
   NormParams p = norm_params(h, h_dtype, h_stride, gate, gate_dtype, gate_stride, act, w_post, res, res_dtype,
                              res_stride, scale, w_pre, eps, N, D);
@@ -254,6 +268,9 @@ int pararnn_block_norm_adjoint(const void* h, int h_dtype, long long h_stride, c
   p.dg = dgate;
   p.dres = dres;
   p.part = static_cast<float*>(workspace);
+  p.status = status;
+  wait_opts(opts, p.wait_ns, p.withhold);
+  if (!clear_status(status, (cudaStream_t)stream)) return PARARNN_ERR_CUDA;
   return done(launch_norm_bwd(p, dw_post, dscale, dw_pre, (cudaStream_t)stream));
 }
 

@@ -281,7 +281,6 @@ __device__ __forceinline__ void copy_bulk(uint32_t dst, const void* src, unsigne
                "l"(src), "r"(bytes), "r"(smem_u32(bar))
                : "memory");
 }
-constexpr uint64_t kNormWaitNs = 2000000000ull;
 
 // One tensor of the adjoint's ring: the next row to copy (of a narrow row, this
 // thread's channels of it), the bytes to the one after, and where it lies in a
@@ -366,8 +365,10 @@ __global__ void __launch_bounds__(512) norm_bwd(const NormParams p, const int tp
     }
     r.at += r.step;
   };
+  constexpr unsigned kNever = 0xffffffffu;
+  unsigned lost_at = kNever;  // the row whose wait ran out
   auto copy = [&](long long row, int k) {  // the next row, into slot k
-    const bool in = row < p.N;
+    const bool in = row < p.N && (kNarrow || (row != p.withhold && lost_at == kNever));
     if (!kNarrow && in) mbar_arrive_expect_tx(&full[k], bytes);
     copy1(th, kH32, true, in, k);
     copy1(tg, kG32, gate, in, k);
@@ -387,11 +388,12 @@ __global__ void __launch_bounds__(512) norm_bwd(const NormParams p, const int tp
     return raw_get(v, es == 4);
   };
   // Until row r is in slot k; of narrow rows, all but the S - 2 latest copies.
-  // A wait that runs out makes the rest of the block's rows NaN.
-  bool lost = false;
+  // A thread whose wait runs out is lost: it waits no more, its part of the rows'
+  // sums is NaN from there on (so all that depends on them is, in every thread),
+  // it fills its own channels with NaN at the end, and thread 0 copies no more.
   auto wait = [&](unsigned r, int k) {
     if (!kNarrow) {
-      if (!lost) lost = !mbar_wait_bounded(&full[k], (r / S) & 1, kNormWaitNs);
+      if (lost_at == kNever && !mbar_wait_bounded(&full[k], (r / S) & 1, p.wait_ns)) lost_at = r;
     } else if (S == 4) {
       asm volatile("cp.async.wait_group 2;" ::: "memory");
     } else if (S == 3) {
@@ -420,7 +422,7 @@ __global__ void __launch_bounds__(512) norm_bwd(const NormParams p, const int tp
   float kh1 = 1.f;  // 1 / rms(h) of the row at hand
   auto first_norm = [&](unsigned r, int k) {
     wait(r, k);
-    float q[6] = {squares(k), 0.f, 0.f, 0.f, 0.f, 0.f};
+    float q[6] = {lost_at != kNever ? __int_as_float(0x7fffffff) : squares(k), 0.f, 0.f, 0.f, 0.f, 0.f};
     row_sum6<kNarrow>(q, tpr, sh, buf);
     kh1 = rsqrtf(fmaf(q[0], invD, p.eps));
   };
@@ -474,6 +476,8 @@ __global__ void __launch_bounds__(512) norm_bwd(const NormParams p, const int tp
       }
     }
     if (ahead || (kNarrow && post)) q[5] = squares(next);
+    const bool lost = !kNarrow && lost_at != kNever;
+    if (lost) (pre ? q[0] : q[2]) = q[5] = __int_as_float(0x7fffffff);
     row_sum6<kNarrow>(q, tpr, sh, buf);
     // every thread is done with the row before: its slot takes a row again
     if (!kNarrow && S > 1 && threadIdx.x == 0) copy(row + (S - 1) * step, at == 0 ? S - 1 : at - 1);
@@ -495,7 +499,6 @@ __global__ void __launch_bounds__(512) norm_bwd(const NormParams p, const int tp
         ap[i].v[j] = lfma(dx.v[j], sn, ap[i].v[j]);
         d.v[j] = lfma(k, lfma(sn, nmean, lmul(dx.v[j], w.v[j])), d.v[j]);
       }
-      if (lost) d = {both(__int_as_float(0x7fffffff)), d.v[1], d.v[2], d.v[3]};
       if (p.dres && ok) store8(p.dres, row * p.D + c, f32<TP>(p, kR32), d);
       if (gate) {
         const F8 g = get(tg, kG32, i, at);
@@ -528,7 +531,6 @@ __global__ void __launch_bounds__(512) norm_bwd(const NormParams p, const int tp
     at = next;
   }
   if (kNarrow) asm volatile("cp.async.wait_group 0;" ::: "memory");
-  if (!p.part) return;
   // [blocks][parts with a weight][D]: w_post, scale, w_pre
   const int n = (post ? 1 : 0) + (scale ? 1 : 0) + (pre ? 1 : 0);
   float* const out = p.part + (size_t)blockIdx.x * n * p.D;
@@ -536,14 +538,32 @@ __global__ void __launch_bounds__(512) norm_bwd(const NormParams p, const int tp
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = 8 * (i * tpr + t);
-      if (c >= p.D) continue;
+      if (c >= p.D || !p.part) continue;
       float* q = out + c;
       if (post) store8(q, 0, true, aw[i]), q += p.D;
       if (scale) store8(q, 0, true, as[i]), q += p.D;
       if (pre) store8(q, 0, true, ap[i]);
     }
+    if (lost_at == kNever) return;
+    // what a lost thread wrote since, again
+    if (p.status) *p.status = PARARNN_STATUS_TIMEOUT;
+    const float2 nan = both(__int_as_float(0x7fffffff));
+    const F8 nans = {nan, nan, nan, nan};
+    for (int c = 8 * t; c < p.D; c += 8 * tpr) {
+      for (row = blockIdx.x + lost_at * step; row < p.N; row += step) {
+        if (p.dres) store8(p.dres, row * p.D + c, f32<TP>(p, kR32), nans);
+        if (gate) store8(p.dg, row * p.D + c, f32<TP>(p, kG32), nans);
+        store8(p.dh, row * p.D + c, f32<TP>(p, kH32), nans);
+      }
+      for (int i = 0; i < n && p.part; ++i) store8(out + i * p.D, c, true, nans);
+    }
+    // The block's shared memory must outlive its copies: of the rows from the
+    // one lost on, S at most were copied (the waits for others run out).
+    if (threadIdx.x == 0)
+      for (unsigned r = lost_at; r < lost_at + S; ++r) mbar_wait_bounded(&full[r % S], (r / S) & 1, p.wait_ns);
     return;
   }
+  if (!p.part) return;
   // several rows a block: its slots' sums, in their order
   float* const acc = reinterpret_cast<float*>(smem);  // [n][slots x 8 tpr]: 2048 channels each (256 threads of 8)
   const int width = 8 * tpr;

@@ -19,6 +19,9 @@ struct NormParams {
   float eps;
   long long N;
   int D;
+  int* status;                 // adjoint: device word for a wait that ran out, or NULL
+  unsigned long long wait_ns;  // adjoint: bound on a wait for a row's copies
+  int withhold;                // testing: the row that is not copied; -1: none
 };
 
 int norm_max_d();

@@ -33,6 +33,16 @@ def _cases():
         C["adjoint_" + name] = ("pararnn_linrec_adjoint_ex", list(a.values()), want)
     adj("status_misaligned", -5, status=0x2001)
     adj("ws_too_small", -3, wsb=64)
+
+    def nadj(name, want, **o):
+        a = dict(h=0x1000, hd=pr.PARARNN_F32, lh=64, g=None, gd=0, lg=0, act=0, wpost=None, r=None, rd=0, lr=0,
+                 sc=None, wpre=0x2000, ds=0x3000, dsd=bf16, lds=64, dx=0x4000, dxd=bf16, ldx=64, dh=0x5000,
+                 dg=None, dres=None, dwpost=None, dsc=None, dwpre=None, eps=1e-6, N=2, D=64, status=None,
+                 ws=0x10000, wsb=1 << 22, opts=None, stream=None)
+        a.update(o)
+        C["norm_adjoint_" + name] = ("pararnn_block_norm_adjoint_ex", list(a.values()), want)
+    nadj("status_misaligned", -5, status=0x2001)
+    nadj("ws_too_small", -3, wsb=16)
     return C
 
 

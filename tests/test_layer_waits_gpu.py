@@ -132,3 +132,56 @@ def test_status_in_a_graph_and_through_the_plain_bindings(cuda_ok):
         pr.linrec_solve(DECAY, **x, status=torch.zeros(1, device="cuda"))
     with pytest.raises(ValueError):
         pr.linrec_solve(DECAY, **x, status=torch.zeros(1, dtype=torch.int32))
+
+
+# rings of four rows, three, two and one; a norm first, a norm last, neither
+NORMS = {"full": (dict(gate=1, post=1, res=1, scale=1, pre=1), (1000, 4096, 8192)),
+         "pre": (dict(res=1, pre=1), (520, 4096)), "post": (dict(gate=1, post=1), (1000, 8192)),
+         "plain": (dict(gate=1, scale=1), (1000,))}
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("kind,D", [(k, D) for k, (_, Ds) in NORMS.items() for D in Ds])
+def test_norm_adjoint_whose_copies_never_come(cuda_ok, kind, D, dtype):
+    parts, N = NORMS[kind][0], 4000     # several rows a block, at any width
+    gen = torch.Generator().manual_seed(D)
+    r = lambda *s: torch.randn(s, generator=gen)  # noqa: E731
+    row = lambda k: r(N, D).to(dtype).cuda() if parts.get(k) else None  # noqa: E731
+    vec = lambda k: (1 + 0.1 * r(D)).cuda() if parts.get(k) else None  # noqa: E731
+    p = dict(gate=row("gate"), w_post=vec("post"), res=row("res"), scale=vec("scale"), w_pre=vec("pre"))
+    h, ds, dx = r(N, D).cuda(), r(N, D).to(dtype).cuda(), row("pre")
+    st = word()
+    want = pr.block_norm_adjoint(h, ds, dx, **p, status=st)
+    assert st.item() == 0
+    for at in (0, 700, 3999):
+        got = pr.block_norm_adjoint(h, ds, dx, **p, status=st, opts=withhold(at))
+        torch.cuda.synchronize()
+        assert st.item() == TIMEOUT
+        for k in ("dh", "dgate", "dres"):
+            if got[k] is None:
+                continue
+            lost = torch.isnan(got[k])
+            rows = lost.any(-1)
+            # whole rows: the one withheld and some that the block had after it
+            # (or, where a row's wait is taken a row ahead, the one before it)
+            assert rows[at] and torch.equal(rows, lost.all(-1)), k
+            assert torch.equal(got[k][~rows], want[k][~rows]), k
+            assert int(rows.sum()) < N // 20, k
+        for k in ("dw_post", "dscale", "dw_pre"):
+            assert got[k] is None or torch.isnan(got[k]).all(), k
+        again = pr.block_norm_adjoint(h, ds, dx, **p, status=st)
+        assert st.item() == 0
+        assert all(again[k] is None or torch.equal(again[k], want[k]) for k in again)
+
+
+def test_norm_adjoint_status_through_the_plain_binding(cuda_ok):
+    N, D = 600, 520
+    h, ds, w = torch.randn(N, D, device="cuda"), torch.randn(N, D, device="cuda"), torch.ones(D, device="cuda")
+    ws = torch.empty(pr.pararnn_block_norm_workspace_size(N, D), dtype=torch.uint8, device="cuda")
+    dh, dw, st = torch.empty_like(h), torch.empty_like(w), word()
+    for opts, want in ((None, 0), (withhold(1), TIMEOUT), (None, 0)):
+        pr.pararnn_block_norm_adjoint_ex(h, D, None, 0, 0, w, None, 0, None, None, ds, D, None, 0, dh, None,
+                                         None, dw, None, None, 1e-6, N, D, st, ws, opts)
+        assert st.item() == want and bool(torch.isnan(dh).any()) == (want != 0)
+    ref = pr.block_norm_adjoint(h, ds, None, w_post=w)
+    assert torch.equal(dh, ref["dh"]) and torch.equal(dw, ref["dw_post"])

@@ -22,6 +22,7 @@
 #include "block_norm.cuh"
 #include "colsum.cuh"
 #include "linrec_cell.cuh"
+#include "smem_once.cuh"
 
 namespace pararnn {
 namespace {

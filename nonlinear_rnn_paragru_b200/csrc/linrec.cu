@@ -28,6 +28,7 @@
 
 #include "colsum.cuh"
 #include "linrec_cell.cuh"
+#include "smem_once.cuh"
 
 namespace cg = cooperative_groups;
 

@@ -206,21 +206,6 @@ __device__ __forceinline__ float2 bf16_pair(unsigned v) {
   return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
 }
 
-// A kernel's leave to use more dynamic shared memory than the default, asked for
-// once on each device (a call of its own costs about a microsecond).
-struct SmemOnce {
-  int bytes[64] = {};
-  int allow(const void* kernel, int most) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return (int)e;
-    if (dev < 64 && bytes[dev] >= most) return 0;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-    if (e == cudaSuccess && dev < 64) bytes[dev] = most;
-    return (int)e;
-  }
-};
-
 struct LinParams {
   const void* u;
   long long sb, st, sg;  // strides of u in elements: batch row, step, gate

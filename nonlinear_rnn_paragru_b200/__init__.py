@@ -172,6 +172,14 @@ def _wptr(t):
     return _ptr(t, None)
 
 
+def _mptr(t):
+    """Device pointer of a mask of bytes: elements of any other size would be
+    read as several."""
+    if t is not None and not isinstance(t, int) and t.dtype not in (torch.bool, torch.uint8):
+        raise TypeError(f"pararnn expects a mask of torch.bool or torch.uint8, got {t.dtype}")
+    return _ptr(t, None)
+
+
 def _stream(stream):
     if stream is None:
         return torch.cuda.current_stream().cuda_stream
@@ -607,14 +615,14 @@ def pararnn_linrec_solve(cell, u, lam, bias, h0, reset, h, kappa=8.0, stream=Non
     B, T, G, D = u.shape
     _check(load_library().pararnn_linrec_solve(
         cell, u.data_ptr(), _code(u), *_lin_u(cell, u, 4)[2], _ptr(lam), _ptr(bias), _ptr(h0),
-        _ptr(reset, None), _ptr(h), B, T, D, kappa, _stream(stream)), "pararnn_linrec_solve")
+        _mptr(reset), _ptr(h), B, T, D, kappa, _stream(stream)), "pararnn_linrec_solve")
 
 
 def pararnn_linrec_solve_ex(cell, u, lam, bias, h0, reset, h, status, opts, kappa=8.0, stream=None):
     B, T, G, D = u.shape
     _check(load_library().pararnn_linrec_solve_ex(
         cell, u.data_ptr(), _code(u), *_lin_u(cell, u, 4)[2], _ptr(lam), _ptr(bias), _ptr(h0),
-        _ptr(reset, None), _ptr(h), B, T, D, kappa, _iptr(status),
+        _mptr(reset), _ptr(h), B, T, D, kappa, _iptr(status),
         ctypes.byref(opts) if opts is not None else None, _stream(stream)),
         "pararnn_linrec_solve_ex")
 
@@ -628,7 +636,7 @@ def pararnn_linrec_adjoint(cell, u, lam, bias, h0, reset, h, dLdh, du, dlam, dbi
     B, T, G, D = u.shape
     _check(load_library().pararnn_linrec_adjoint(
         cell, u.data_ptr(), _code(u), *_lin_u(cell, u, 4)[2], _ptr(lam), _ptr(bias), _ptr(h0),
-        _ptr(reset, None), _ptr(h), _ptr(dLdh), _ptr(du, None), _code(du), _ptr(dlam),
+        _mptr(reset), _ptr(h), _ptr(dLdh), _ptr(du, None), _code(du), _ptr(dlam),
         _ptr(dbias), _ptr(dh0), B, T, D, kappa, _wptr(workspace),
         workspace.numel() * workspace.element_size(), _stream(stream)),
         "pararnn_linrec_adjoint")
@@ -639,7 +647,7 @@ def pararnn_linrec_adjoint_ex(cell, u, lam, bias, h0, reset, h, dLdh, du, dlam, 
     B, T, G, D = u.shape
     _check(load_library().pararnn_linrec_adjoint_ex(
         cell, u.data_ptr(), _code(u), *_lin_u(cell, u, 4)[2], _ptr(lam), _ptr(bias), _ptr(h0),
-        _ptr(reset, None), _ptr(h), _ptr(dLdh), _ptr(du, None), _code(du), _ptr(dlam),
+        _mptr(reset), _ptr(h), _ptr(dLdh), _ptr(du, None), _code(du), _ptr(dlam),
         _ptr(dbias), _ptr(dh0), B, T, D, kappa, _iptr(status), _wptr(workspace),
         workspace.numel() * workspace.element_size(),
         ctypes.byref(opts) if opts is not None else None, _stream(stream)),

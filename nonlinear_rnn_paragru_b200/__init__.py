@@ -762,11 +762,20 @@ def _any_ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _rptr(t):
+    """Device pointer of rows that may lie apart (None -> NULL)."""
+    if t is None:
+        return None
+    if not t.is_cuda or (t.stride(-1) != 1 and t.shape[-1] > 1):
+        raise ValueError("pararnn expects CUDA tensors with contiguous channels")
+    return t.data_ptr()
+
+
 def pararnn_block_norm(h, h_stride, gate, gate_stride, act, w_post, res, res_stride, scale, w_pre, s,
                        x, eps, N, D, stream=None):
     _check(load_library().pararnn_block_norm(
-        h.data_ptr(), _code(h), h_stride, _any_ptr(gate), _code(gate), gate_stride, act, _ptr(w_post),
-        _any_ptr(res), _code(res), res_stride, _ptr(scale), _ptr(w_pre), _ptr(s, None), _code(s),
+        _rptr(h), _code(h), h_stride, _rptr(gate), _code(gate), gate_stride, act, _ptr(w_post),
+        _rptr(res), _code(res), res_stride, _ptr(scale), _ptr(w_pre), _ptr(s, None), _code(s),
         _ptr(x, None), _code(x), eps, N, D, _stream(stream)), "pararnn_block_norm")
 
 
@@ -778,9 +787,9 @@ def pararnn_block_norm_adjoint(h, h_stride, gate, gate_stride, act, w_post, res,
                                w_pre, ds, ds_stride, dx, dx_stride, dh, dgate, dres, dw_post, dscale,
                                dw_pre, eps, N, D, workspace, stream=None):
     _check(load_library().pararnn_block_norm_adjoint(
-        h.data_ptr(), _code(h), h_stride, _any_ptr(gate), _code(gate), gate_stride, act, _ptr(w_post),
-        _any_ptr(res), _code(res), res_stride, _ptr(scale), _ptr(w_pre), _any_ptr(ds), _code(ds),
-        ds_stride, _any_ptr(dx), _code(dx), dx_stride, _ptr(dh, None), _ptr(dgate, None),
+        _rptr(h), _code(h), h_stride, _rptr(gate), _code(gate), gate_stride, act, _ptr(w_post),
+        _rptr(res), _code(res), res_stride, _ptr(scale), _ptr(w_pre), _rptr(ds), _code(ds),
+        ds_stride, _rptr(dx), _code(dx), dx_stride, _ptr(dh, None), _ptr(dgate, None),
         _ptr(dres, None), _ptr(dw_post), _ptr(dscale), _ptr(dw_pre), eps, N, D, _wptr(workspace),
         workspace.numel() * workspace.element_size(), _stream(stream)),
         "pararnn_block_norm_adjoint")
@@ -790,9 +799,9 @@ def pararnn_block_norm_adjoint_ex(h, h_stride, gate, gate_stride, act, w_post, r
                                   w_pre, ds, ds_stride, dx, dx_stride, dh, dgate, dres, dw_post, dscale,
                                   dw_pre, eps, N, D, status, workspace, opts, stream=None):
     _check(load_library().pararnn_block_norm_adjoint_ex(
-        h.data_ptr(), _code(h), h_stride, _any_ptr(gate), _code(gate), gate_stride, act, _ptr(w_post),
-        _any_ptr(res), _code(res), res_stride, _ptr(scale), _ptr(w_pre), _any_ptr(ds), _code(ds),
-        ds_stride, _any_ptr(dx), _code(dx), dx_stride, _ptr(dh, None), _ptr(dgate, None),
+        _rptr(h), _code(h), h_stride, _rptr(gate), _code(gate), gate_stride, act, _ptr(w_post),
+        _rptr(res), _code(res), res_stride, _ptr(scale), _ptr(w_pre), _rptr(ds), _code(ds),
+        ds_stride, _rptr(dx), _code(dx), dx_stride, _ptr(dh, None), _ptr(dgate, None),
         _ptr(dres, None), _ptr(dw_post), _ptr(dscale), _ptr(dw_pre), eps, N, D, _iptr(status),
         _wptr(workspace), workspace.numel() * workspace.element_size(),
         ctypes.byref(opts) if opts is not None else None, _stream(stream)),

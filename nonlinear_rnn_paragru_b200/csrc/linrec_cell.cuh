@@ -68,12 +68,14 @@ __device__ __forceinline__ float2 decay_nm(float2 v) {
   return make_float2(v.x < 0.36f ? p.x : e.x, v.y < 0.36f ? p.y : e.y);
 }
 
-// -tanh y and R = 1 / (1 + e^2y), of which 1 - tanh^2 = 4 (R - R^2).  Below
-// |y| = 0.2 the Taylor series to y^7 (the next term is below 2^-24 of the sum
-// there); above, 2 R - 1, whose rounding is 2^-23 at most (10 units of the
-// last place of the smallest |tanh| it serves).
-__device__ __forceinline__ float2 minus_tanh(float2 y, float2& R) {
-  R = rcp_2(ladd(ex2_2(lmul(y, both(2.f * kLog2e))), both(1.f)));
+// -tanh y and its slope 1 - tanh^2 = 4 t R^2 with t = e^2y, R = 1 / (1 + t): of
+// its own size on both sides (4 (R - R^2) would be 0 from y = -8.5 down, where R
+// rounds to 1).  -tanh below |y| = 0.2 is the Taylor series to y^7 (the next term
+// is below 2^-24 of the sum there); above, 2 R - 1, whose rounding is 2^-23 at
+// most (10 units of the last place of the smallest |tanh| it serves).
+__device__ __forceinline__ float2 minus_tanh(float2 y, float2& slope) {
+  const float2 t = ex2_2(lmul(y, both(2.f * kLog2e))), R = rcp_2(ladd(t, both(1.f)));
+  slope = lmul(lmul(lmul(finite(t), R), R), both(4.f));
   const float2 big = lfma(R, both(2.f), both(-1.f));
   const float2 s = lmul(y, y);
   float2 p = lfma(s, both(17.f / 315.f), both(-2.f / 15.f));
@@ -106,9 +108,9 @@ struct LinCell<PARARNN_LIN_GRU> {
   }
   __device__ __forceinline__ float2 zarg(float2 u) const { return lfma(u, both(-kLog2e), bz); }
   __device__ __forceinline__ void coef(const float2 (&u)[G], float2& nm, float2& b) const {
-    float2 R;
+    float2 slope;
     nm = rcp_2(neg2(ladd(ex2_2(zarg(u[0])), both(1.f))));  // -z; 0 where 2^v overflows
-    b = lmul(nm, minus_tanh(ladd(u[1], bc), R));
+    b = lmul(nm, minus_tanh(ladd(u[1], bc), slope));
   }
   // The adjoint's first pass: nm from the first gate, and what the second
   // keeps of it: z (1 - z), of its own size where z is near 1 too.
@@ -121,10 +123,10 @@ struct LinCell<PARARNN_LIN_GRU> {
   // The second: du of one step from lambda and h_{t-1}.
   __device__ __forceinline__ void grad(const float2 (&u)[G], float2 nm, const float2 (&keep)[kKeep], float2 hp,
                                        float2 lt, float2 (&du)[G], float2& /*e*/) const {
-    float2 R;
-    const float2 nc = minus_tanh(ladd(u[1], bc), R), nl = neg2(lt);
+    float2 slope;
+    const float2 nc = minus_tanh(ladd(u[1], bc), slope), nl = neg2(lt);
     du[0] = lmul(lmul(nl, keep[0]), ladd(hp, nc));
-    du[1] = lmul(lmul(nl, nm), lmul(lfma(neg2(R), R, R), both(4.f)));
+    du[1] = lmul(lmul(nl, nm), slope);
   }
   static __device__ __forceinline__ float2 lam_scale(const float*, int) { return both(0.f); }
 };

@@ -95,8 +95,10 @@ def lin_adjoint(cell, u, lam, bias, h0, h, g, reset=None, kappa=8.0, delta=48 * 
     p = u + (0 if bias is None else bias)
     if cell == LIN_GRU:
         z, zc, c = _sig(p[..., 0, :]), _sig(-p[..., 0, :]), np.tanh(p[..., 1, :])
-        f = np.stack([(c - hp) * z * zc, z * (1 - c * c)], 2)
-        a = np.stack([(np.abs(c) + np.abs(hp)) * z * zc, z * (1 + c * c)], 2)
+        t = np.exp(-2 * np.abs(p[..., 1, :]))       # 1 - tanh^2 of its own size: no cancellation is allowed for
+        slope = z * 4 * t / (1 + t) ** 2
+        f = np.stack([(c - hp) * z * zc, slope], 2)
+        a = np.stack([(np.abs(c) + np.abs(hp)) * z * zc, slope], 2)
         ef = ea = None
     else:
         r, rc = _sig(p[..., 0, :]), _sig(-p[..., 0, :])

@@ -1,0 +1,46 @@
+"""The gated linear recurrence's adjoint where its gates saturate."""
+import numpy as np
+import pytest
+import torch
+
+import nonlinear_rnn_paragru_b200 as pr
+from oracle import layer as ol
+
+pytestmark = pytest.mark.gpu
+
+GRU, DECAY = pr.PARARNN_LIN_GRU, pr.PARARNN_LIN_DECAY
+
+
+def within(got, want, err):
+    got = got.double().cpu().numpy()
+    bad = ~(np.abs(got - want) <= err + 1e-37)      # a NaN is off too
+    assert not bad.any(), (float((np.abs(got - want) / (err + 1e-37)).max()), np.argwhere(bad)[:3])
+
+
+@pytest.mark.parametrize("T", [1, 37, 900])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_candidates_far_out_have_their_gradient(cuda_ok, sign, T):
+    # |y| of 7 to 10.  An fp32 slope 4 t / (1 + t)^2, t = e^2y: three roundings of 2y (20) make 60, ex2, the
+    # reciprocal, 1 + t and the products 11 more; z (arguments up to 6: 24) and lambda's factors 5: 100
+    # roundings, below 2 x 64
+    B, D = 2, 72
+    g = torch.Generator().manual_seed(T)
+    u = torch.randn((B, T, 2, D), generator=g).clamp_(-5, 5)
+    u[:, :, 1] = sign * (7 + 3 * torch.rand((B, T, D), generator=g))
+    h0, dLdh = torch.randn((B, D), generator=g), torch.randn((B, T, D), generator=g)
+    u, h0, dLdh = u.cuda(), h0.cuda(), dLdh.cuda()
+    h = pr.linrec_solve(GRU, u, h0=h0)
+    got = pr.linrec_adjoint(GRU, u, None, None, h0, h, dLdh)
+    want = ol.lin_adjoint(GRU, u, None, None, h0, h, dLdh, delta=64 * 2.0 ** -24)
+    for k in ("du", "dbias", "dh0"):
+        within(got[k], *want[k])
+    # and nowhere is it rounded away
+    assert (got["du"][:, :, 1] != 0).all()
+
+
+def test_infinite_candidates_have_no_gradient(cuda_ok):
+    u = torch.zeros((1, 3, 2, 8), device="cuda")
+    u[:, :, 1, :4], u[:, :, 1, 4:] = float("inf"), float("-inf")
+    h = pr.linrec_solve(GRU, u)
+    got = pr.linrec_adjoint(GRU, u, None, None, None, h, torch.ones_like(h))
+    assert (got["du"][:, :, 1] == 0).all() and torch.isfinite(got["du"]).all()

@@ -165,7 +165,8 @@ struct LinCell<PARARNN_LIN_DECAY> {
   __device__ __forceinline__ void grad(const float2 (&u)[G], float2 nm, const float2 (&keep)[kKeep], float2 hp,
                                        float2 lt, float2 (&du)[G], float2& e) const {
     const float2 t = ex2_2(lfma(u[1], both(-kLog2e), bi)), i = rcp_2(ladd(t, both(1.f)));
-    const float2 x = ladd(u[2], bx), a = ladd(nm, both(1.f)), w = keep[0];
+    // a from w, since 1 + nm is off by 2^-24 of 1, not of a
+    const float2 x = ladd(u[2], bx), w = keep[0], a = ex2_2(lmul(w, both(-kLog2e)));
     const float2 s = lmul(neg2(nm), ladd(nm, both(2.f)));  // beta^2
     // 1 / beta; w / beta -> 0 with w
     const float2 rb = make_float2(s.x >= 1.1754944e-38f ? rsqrt_apx(s.x) : 0.f,

@@ -44,3 +44,21 @@ def test_infinite_candidates_have_no_gradient(cuda_ok):
     h = pr.linrec_solve(GRU, u)
     got = pr.linrec_adjoint(GRU, u, None, None, None, h, torch.ones_like(h))
     assert (got["du"][:, :, 1] == 0).all() and torch.isfinite(got["du"]).all()
+
+
+@pytest.mark.parametrize("T", [1, 33, 700])
+def test_channels_that_forget_at_once_have_their_gradient(cuda_ok, T):
+    # w = -log a up to 8 softplus(3) = 24.4, a down to 2.5e-11.  An fp32 w is off by up to 24 roundings of its
+    # sigmoid, 6 of softplus and the products: a by 24.4 x 30 of itself, and the gradient of r by that and
+    # the 48 roundings of its other factors: 780
+    B, D = 2, 72
+    g = torch.Generator().manual_seed(T)
+    u = torch.randn((B, T, 3, D), generator=g).clamp_(-5, 5).cuda()
+    u[:, :, 0] = u[:, :, 0].abs()
+    lam = torch.linspace(-4, 3, D).cuda()
+    h0, dLdh = torch.randn((B, D), generator=g).cuda(), torch.randn((B, T, D), generator=g).cuda()
+    h = pr.linrec_solve(DECAY, u, lam, h0=h0)
+    got = pr.linrec_adjoint(DECAY, u, lam, None, h0, h, dLdh)
+    want = ol.lin_adjoint(DECAY, u, lam, None, h0, h, dLdh, delta=780 * 2.0 ** -24)
+    for k in ("du", "dlam", "dbias"):
+        within(got[k], *want[k])

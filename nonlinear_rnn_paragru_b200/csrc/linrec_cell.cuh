@@ -87,10 +87,11 @@ __device__ __forceinline__ float2 minus_tanh(float2 y, float2& slope) {
 
 // log(1 + e^x), once per channel
 __device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); }
-// its logarithm's derivative sig(x) / softplus(x); 1 where e^x underflows
+// its logarithm's derivative sig(x) / softplus(x), by e^-|x|, which does not
+// overflow; 1 where e^x underflows
 __device__ __forceinline__ float dlog_softplus(float x) {
-  const float sp = softplus(x);
-  return sp > 0.f ? 1.f / (1.f + expf(-x)) / sp : 1.f;
+  const float sp = softplus(x), e = expf(-fabsf(x));
+  return sp > 0.f ? (x < 0.f ? e : 1.f) / ((1.f + e) * sp) : 1.f;
 }
 
 __device__ __forceinline__ float2 vec2(const float* p, int d) { return p ? make_float2(p[d], p[d + 1]) : both(0.f); }

@@ -62,3 +62,21 @@ def test_channels_that_forget_at_once_have_their_gradient(cuda_ok, T):
     want = ol.lin_adjoint(DECAY, u, lam, None, h0, h, dLdh, delta=780 * 2.0 ** -24)
     for k in ("du", "dlam", "dbias"):
         within(got[k], *want[k])
+
+
+def test_lam_where_its_softplus_is_denormal(cuda_ok):
+    # softplus(-95) is 5.5e-42, some 3900 of fp32's smallest step: expf, log1pf and their quotient are off by
+    # 3 steps of 3900, the products with kappa, log2 e, r and ln 2 by less: 2e-3 covers them
+    T, D = 40, 72
+    g = torch.Generator().manual_seed(1)
+    u = torch.zeros((1, T, 3, D))                     # x = 0: the states are h0's, and the first term is 0
+    u[:, :, 0] = torch.randn((1, T, D), generator=g).abs().clamp_(0, 5)
+    u = u.cuda()
+    h0 = 1e10 * (1 + torch.rand((1, D), generator=g)).cuda()
+    dLdh = 1e10 * (1 + torch.rand((1, T, D), generator=g)).cuda()
+    for x in (-88.0, -92.0, -95.0):
+        lam = torch.full((D,), x, device="cuda")
+        h = pr.linrec_solve(DECAY, u, lam, h0=h0)
+        got = pr.linrec_adjoint(DECAY, u, lam, None, h0, h, dLdh)["dlam"].double().cpu().numpy()
+        want = ol.lin_adjoint(DECAY, u, lam, None, h0, h, dLdh)["dlam"][0]
+        assert (np.abs(got - want) <= 2e-3 * np.abs(want)).all(), (x, float(got[0]), float(want[0]))

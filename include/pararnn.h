@@ -500,6 +500,8 @@ int pararnn_lstm_step(const void* u_t, int u_dtype, const float* a,
  * u[b * u_stride_b + t * u_stride_t + q * u_stride_g + d].  The strides are
  * multiples of 8 elements and >= 0, u is 16-byte aligned.
  * kappa > 0 and finite (ignored for PARARNN_LIN_GRU).
+ * D % 8 == 0; T and D up to 2^30, B * T * D up to 2^40, and B * D below 2^31
+ * but for the step (else PARARNN_ERR_TOO_LARGE).
  * The states are fp32 throughout.  Results do not depend on timing: equal
  * calls return equal bits.  Outputs must not overlap inputs, but for
  * h_next == h_prev of the step. */

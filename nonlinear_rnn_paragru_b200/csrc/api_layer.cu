@@ -39,6 +39,14 @@ bool clear_status(int* status, cudaStream_t stream) {
 
 bool stride_ok(long long s) { return s >= 0 && s % 8 == 0; }
 
+// Sizes whose indexes and grids fit the kernels' types: B * T * D <= 2^40 (as a
+// division, since the product can pass 64 bits), T and D <= 2^30
+bool lin_fits(int B, int T, int D) {
+  return T <= (1 << 30) && D <= (1 << 30) && (long long)B * T <= (1LL << 40) / D;
+}
+// and of the scans
+bool scan_fits(int B, int T, int D) { return lin_fits(B, T, D) && linrec_most_ctas(B, D) < (1LL << 31); }
+
 // what the three recurrence calls check alike; T = 1 for the step
 int lin_args(int cell, const void* u, int u_dtype, long long sb, long long st, long long sg, const float* lam,
              const float* bias, int B, int T, int D, float kappa) {
@@ -48,7 +56,7 @@ int lin_args(int cell, const void* u, int u_dtype, long long sb, long long st, l
   if (!u || (cell == PARARNN_LIN_DECAY) != (lam != nullptr)) return PARARNN_ERR_INVALID_ARG;
   if (cell == PARARNN_LIN_DECAY && !(kappa > 0.f && std::isfinite(kappa))) return PARARNN_ERR_INVALID_ARG;
   if (!stride_ok(sb) || !stride_ok(st) || !stride_ok(sg)) return PARARNN_ERR_INVALID_ARG;
-  if ((long long)B * T * D > (1LL << 40) || T > (1 << 30)) return PARARNN_ERR_TOO_LARGE;
+  if (!lin_fits(B, T, D)) return PARARNN_ERR_TOO_LARGE;
   if (!aligned(u, 16) || (lam && !aligned(lam, 4)) || (bias && !aligned(bias, 4))) return PARARNN_ERR_MISALIGNED;
   return PARARNN_OK;
 }
@@ -130,7 +138,7 @@ int pararnn_linrec_solve_ex(int cell, const void* u, int u_dtype, long long u_st
   const int rc = lin_args(cell, u, u_dtype, u_stride_b, u_stride_t, u_stride_g, lam, bias, B, T, D, kappa);
   if (rc) return rc;
   if (!h) return PARARNN_ERR_INVALID_ARG;
-  if (linrec_most_ctas(B, D) >= (1LL << 31)) return PARARNN_ERR_TOO_LARGE;
+  if (!scan_fits(B, T, D)) return PARARNN_ERR_TOO_LARGE;
   if (!aligned(h, 16) || (h0 && !aligned(h0, 4)) || (status && !aligned(status, 4))) return PARARNN_ERR_MISALIGNED;
   LinParams p = lin_params(u, u_stride_b, u_stride_t, u_stride_g, lam, bias, h0, reset, B, T, D, kappa);
   p.h = h;
@@ -142,7 +150,7 @@ int pararnn_linrec_solve_ex(int cell, const void* u, int u_dtype, long long u_st
 
 size_t pararnn_linrec_workspace_size(int cell, int B, int T, int D) {
   if (cell != PARARNN_LIN_GRU && cell != PARARNN_LIN_DECAY) return 0;
-  if (B < 1 || T < 1 || D < 1 || D % 8 != 0 || (long long)B * T * D > (1LL << 40) || T > (1 << 30)) return 0;
+  if (B < 1 || T < 1 || D < 1 || D % 8 != 0 || !scan_fits(B, T, D)) return 0;
   return (linrec_part_floats(cell, B, T, D) * sizeof(float) + 255) / 256 * 256;
 }
 
@@ -167,7 +175,7 @@ int pararnn_linrec_adjoint_ex(int cell, const void* u, int u_dtype, long long u_
   if (!h || !dLdh || !du || !workspace || (cell == PARARNN_LIN_GRU && dlam)) return PARARNN_ERR_INVALID_ARG;
   if (!is_dtype(du_dtype) || (du_dtype == PARARNN_BF16 && u_dtype != PARARNN_BF16))
     return PARARNN_ERR_UNSUPPORTED_DTYPE;
-  if (linrec_most_ctas(B, D) >= (1LL << 31)) return PARARNN_ERR_TOO_LARGE;
+  if (!scan_fits(B, T, D)) return PARARNN_ERR_TOO_LARGE;
   if (!aligned(h, 16) || !aligned(dLdh, 16) || !aligned(du, 16) || (h0 && !aligned(h0, 4)) ||
       (dlam && !aligned(dlam, 4)) || (dbias && !aligned(dbias, 4)) || (dh0 && !aligned(dh0, 4)) ||
       (status && !aligned(status, 4)) || !aligned(workspace, 256))

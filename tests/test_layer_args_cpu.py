@@ -24,6 +24,11 @@ def _cases():
         C["solve_" + name] = ("pararnn_linrec_solve_ex", list(a.values()), want)
     solve("status_misaligned", -5, status=0x2002)
     solve("no_h", -1, h=None)
+    # sizes whose products or sums pass 31, 32 or 64 bits on the way
+    solve("D_too_large", -6, T=1, D=(1 << 31) - 8)
+    solve("D_and_T_too_large", -6, T=2, D=(1 << 30) + 8)
+    solve("product_of_2_64", -6, B=1 << 30, T=1 << 30, D=16)
+    solve("B_too_large", -6, B=(1 << 31) - 1, T=1, D=8)
 
     def adj(name, want, **o):
         a = dict(cell=dec, u=0x1000, dt=bf16, sb=128, st=64, sg=32, lam=0x2000, bias=None, h0=None, reset=None,
@@ -33,6 +38,14 @@ def _cases():
         C["adjoint_" + name] = ("pararnn_linrec_adjoint_ex", list(a.values()), want)
     adj("status_misaligned", -5, status=0x2001)
     adj("ws_too_small", -3, wsb=64)
+    adj("D_too_large", -6, T=1, D=(1 << 31) - 8, wsb=1 << 62)
+    adj("product_of_2_64", -6, B=1 << 30, T=1 << 30, D=16, wsb=1 << 62)
+
+    def size(name, want, *a):
+        C["size_" + name] = ("pararnn_linrec_workspace_size", list(a), want)
+    size("D_too_large", 0, gru, 1, 1, (1 << 31) - 8)
+    size("product_of_2_64", 0, dec, 1 << 30, 1 << 30, 16)
+    size("B_too_large", 0, dec, (1 << 31) - 1, 1, 8)
 
     def nadj(name, want, **o):
         a = dict(h=0x1000, hd=pr.PARARNN_F32, lh=64, g=None, gd=0, lg=0, act=0, wpost=None, r=None, rd=0, lr=0,

@@ -514,13 +514,14 @@ def seq_baseline(cell, u, a, bias=None, c0=None, h0=None, stream=None):
 
 
 # ------------------------------------- gated linear recurrence, block norm --
-# These calls check every shape, type and device, since the library sees
-# pointers only; they run on the device of their tensors, whatever the current
-# one is, and allocate what they return (and their scratch) on the stream they
-# launch on, so both live as long as the work in flight, in a captured graph
-# too.  Inputs made on another stream are the caller's to order, as with every
-# CUDA call.  A decode step takes the GPU 2 us, so the checks are written to
-# cost little.
+# The wrappers (linrec_*, block_norm*) check every shape, type and device, since
+# the library sees pointers only; they run on the device of their tensors,
+# whatever the current one is, and allocate what they return (and their scratch)
+# on the stream they launch on, so both live as long as the work in flight, in a
+# captured graph too.  Inputs made on another stream are the caller's to order,
+# as with every CUDA call.  A decode step takes the GPU 2 us, so the checks are
+# written to cost little.  The bindings of the C names take tensors of the
+# current device, and their sizes on trust.
 _F32, _BF16 = torch.float32, torch.bfloat16
 _DTYPES = {_F32: PARARNN_F32, _BF16: PARARNN_BF16}
 _FLOATS = (_F32, _BF16)
@@ -611,7 +612,16 @@ def _lin_params(cell, dev, B, G, D, lam, bias, h0, h0_name="h0"):
             _need(h0, h0_name, (B, D), dev))
 
 
+def _here(*tensors):
+    """The bindings launch on the current device, whose memory they need."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and not isinstance(t, int) and t.device.index != dev:
+            raise ValueError(f"expected a tensor on cuda:{dev}, got {t.device}")
+
+
 def pararnn_linrec_solve(cell, u, lam, bias, h0, reset, h, kappa=8.0, stream=None):
+    _here(u, lam, bias, h0, reset, h)
     B, T, G, D = u.shape
     _check(load_library().pararnn_linrec_solve(
         cell, u.data_ptr(), _code(u), *_lin_u(cell, u, 4)[2], _ptr(lam), _ptr(bias), _ptr(h0),
@@ -619,6 +629,7 @@ def pararnn_linrec_solve(cell, u, lam, bias, h0, reset, h, kappa=8.0, stream=Non
 
 
 def pararnn_linrec_solve_ex(cell, u, lam, bias, h0, reset, h, status, opts, kappa=8.0, stream=None):
+    _here(u, lam, bias, h0, reset, h, status)
     B, T, G, D = u.shape
     _check(load_library().pararnn_linrec_solve_ex(
         cell, u.data_ptr(), _code(u), *_lin_u(cell, u, 4)[2], _ptr(lam), _ptr(bias), _ptr(h0),
@@ -633,6 +644,7 @@ def pararnn_linrec_workspace_size(cell, B, T, D) -> int:
 
 def pararnn_linrec_adjoint(cell, u, lam, bias, h0, reset, h, dLdh, du, dlam, dbias, dh0,
                            workspace, kappa=8.0, stream=None):
+    _here(u, lam, bias, h0, reset, h, dLdh, du, dlam, dbias, dh0, workspace)
     B, T, G, D = u.shape
     _check(load_library().pararnn_linrec_adjoint(
         cell, u.data_ptr(), _code(u), *_lin_u(cell, u, 4)[2], _ptr(lam), _ptr(bias), _ptr(h0),
@@ -644,6 +656,7 @@ def pararnn_linrec_adjoint(cell, u, lam, bias, h0, reset, h, dLdh, du, dlam, dbi
 
 def pararnn_linrec_adjoint_ex(cell, u, lam, bias, h0, reset, h, dLdh, du, dlam, dbias, dh0, status,
                               workspace, opts, kappa=8.0, stream=None):
+    _here(u, lam, bias, h0, reset, h, dLdh, du, dlam, dbias, dh0, status, workspace)
     B, T, G, D = u.shape
     _check(load_library().pararnn_linrec_adjoint_ex(
         cell, u.data_ptr(), _code(u), *_lin_u(cell, u, 4)[2], _ptr(lam), _ptr(bias), _ptr(h0),
@@ -655,6 +668,7 @@ def pararnn_linrec_adjoint_ex(cell, u, lam, bias, h0, reset, h, dLdh, du, dlam, 
 
 
 def pararnn_linrec_step(cell, u_t, lam, bias, h_prev, h_next, kappa=8.0, stream=None):
+    _here(u_t, lam, bias, h_prev, h_next)
     B, G, D = u_t.shape
     _check(load_library().pararnn_linrec_step(
         cell, u_t.data_ptr(), _code(u_t), *_lin_u(cell, u_t, 3)[2], _ptr(lam), _ptr(bias),
@@ -773,6 +787,7 @@ def _rptr(t):
 
 def pararnn_block_norm(h, h_stride, gate, gate_stride, act, w_post, res, res_stride, scale, w_pre, s,
                        x, eps, N, D, stream=None):
+    _here(h, gate, w_post, res, scale, w_pre, s, x)
     _check(load_library().pararnn_block_norm(
         _rptr(h), _code(h), h_stride, _rptr(gate), _code(gate), gate_stride, act, _ptr(w_post),
         _rptr(res), _code(res), res_stride, _ptr(scale), _ptr(w_pre), _ptr(s, None), _code(s),
@@ -786,6 +801,8 @@ def pararnn_block_norm_workspace_size(N, D) -> int:
 def pararnn_block_norm_adjoint(h, h_stride, gate, gate_stride, act, w_post, res, res_stride, scale,
                                w_pre, ds, ds_stride, dx, dx_stride, dh, dgate, dres, dw_post, dscale,
                                dw_pre, eps, N, D, workspace, stream=None):
+    _here(h, gate, w_post, res, scale, w_pre, ds, dx, dh, dgate, dres, dw_post, dscale,
+          dw_pre, workspace)
     _check(load_library().pararnn_block_norm_adjoint(
         _rptr(h), _code(h), h_stride, _rptr(gate), _code(gate), gate_stride, act, _ptr(w_post),
         _rptr(res), _code(res), res_stride, _ptr(scale), _ptr(w_pre), _rptr(ds), _code(ds),
@@ -798,6 +815,8 @@ def pararnn_block_norm_adjoint(h, h_stride, gate, gate_stride, act, w_post, res,
 def pararnn_block_norm_adjoint_ex(h, h_stride, gate, gate_stride, act, w_post, res, res_stride, scale,
                                   w_pre, ds, ds_stride, dx, dx_stride, dh, dgate, dres, dw_post, dscale,
                                   dw_pre, eps, N, D, status, workspace, opts, stream=None):
+    _here(h, gate, w_post, res, scale, w_pre, ds, dx, dh, dgate, dres, dw_post, dscale,
+          dw_pre, status, workspace)
     _check(load_library().pararnn_block_norm_adjoint_ex(
         _rptr(h), _code(h), h_stride, _rptr(gate), _code(gate), gate_stride, act, _ptr(w_post),
         _rptr(res), _code(res), res_stride, _ptr(scale), _ptr(w_pre), _rptr(ds), _code(ds),

@@ -1,4 +1,5 @@
-"""The layer bindings refuse host tensors before the library sees a pointer."""
+"""The layer bindings refuse host tensors, and tensors of another device than the
+current one, before the library sees a pointer."""
 import pytest
 import torch
 
@@ -6,11 +7,20 @@ import nonlinear_rnn_paragru_b200 as pr
 
 
 class OnDevice(torch.Tensor):
-    """A host tensor that says it is a CUDA tensor, for the arguments beside the one tested."""
+    """A host tensor that says it lies on the first CUDA device, for the arguments beside the one tested."""
+    index = 0
 
     @property
     def is_cuda(self):
         return True
+
+    @property
+    def device(self):
+        return torch.device("cuda", self.index)
+
+
+class Elsewhere(OnDevice):
+    index = 1
 
 
 def dev(*shape, dtype=torch.float32):
@@ -32,6 +42,7 @@ class Library:
 @pytest.fixture(autouse=True)
 def no_library(monkeypatch):
     monkeypatch.setattr(pr, "load_library", Library)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
 
 
 def norm_args():
@@ -64,3 +75,56 @@ def test_block_norm_adjoint_bindings_refuse(name, bad):
         pr.pararnn_block_norm_adjoint(*a.values(), ws, stream=0)
     with pytest.raises(ValueError):
         pr.pararnn_block_norm_adjoint_ex(*a.values(), None, ws, None, stream=0)
+
+
+B, T, G = 2, 4, 2
+
+
+def solve_args():
+    return dict(u=dev(B, T, G, D), lam=None, bias=dev(G, D), h0=dev(B, D), reset=dev(B, T, dtype=torch.uint8),
+                h=dev(B, T, D))
+
+
+def gradient_args():
+    return dict(solve_args(), dLdh=dev(B, T, D), du=dev(B, T, G, D), dlam=None, dbias=dev(G, D), dh0=dev(B, D))
+
+
+def step_args():
+    return dict(u=dev(B, G, D), lam=None, bias=dev(G, D), h_prev=dev(B, D), h_next=dev(B, D))
+
+
+def _calls():
+    ws = lambda: dev(1 << 20, dtype=torch.uint8)  # noqa: E731
+    word = lambda: dev(1, dtype=torch.int32)  # noqa: E731
+    return {
+        "linrec_solve": lambda: solve_args(),
+        "linrec_solve_ex": lambda: dict(solve_args(), status=word(), opts=None),
+        "linrec_adjoint": lambda: dict(gradient_args(), ws=ws()),
+        "linrec_adjoint_ex": lambda: dict(gradient_args(), status=word(), ws=ws(), opts=None),
+        "linrec_step": lambda: step_args(),
+        "block_norm": lambda: norm_args(),
+        "block_norm_adjoint": lambda: dict(adjoint_args(), ws=ws()),
+        "block_norm_adjoint_ex": lambda: dict(adjoint_args(), status=word(), ws=ws(), opts=None),
+    }
+
+
+CASES = [(c, k) for c, a in _calls().items() for k, v in a().items() if torch.is_tensor(v)]
+
+
+def call(name, args):
+    cell = () if name.startswith("block") else (pr.PARARNN_LIN_GRU,)
+    return getattr(pr, "pararnn_" + name)(*cell, *args.values(), stream=0)
+
+
+@pytest.mark.parametrize("name,arg", CASES)
+def test_bindings_refuse_another_device(name, arg):
+    args = _calls()[name]()
+    args[arg] = args[arg].as_subclass(Elsewhere)
+    with pytest.raises(ValueError):
+        call(name, args)
+
+
+@pytest.mark.parametrize("name", _calls())
+def test_bindings_reach_the_library_otherwise(name):
+    with pytest.raises(AssertionError, match="pararnn_" + name):
+        call(name, _calls()[name]())

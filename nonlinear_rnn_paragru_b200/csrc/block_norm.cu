@@ -108,39 +108,32 @@ struct Act {
 
 constexpr int kNormWarps = 16;  // of a block, at most
 struct NormShared {
-  float red[2][2][kNormWarps];
+  float red[2][kNormWarps];
 };
 // entries of warps that a block does not have stay zero
 __device__ __forceinline__ void norm_start(NormShared& sh) {
-  if (threadIdx.x < 4 * kNormWarps) (&sh.red[0][0][0])[threadIdx.x] = 0.f;
+  if (threadIdx.x < 2 * kNormWarps) (&sh.red[0][0])[threadIdx.x] = 0.f;
   __syncthreads();
 }
 
-// Sums over the threads of a row, the same in every thread of it: shuffles in
+// The sum over the threads of a row, the same in every thread of it: shuffles in
 // a warp, then over the warps' sums.  `buf` alternates from call to call, so
 // one barrier a call is enough.
-template <int NVAL>
-__device__ __forceinline__ void row_sum(float (&v)[NVAL], int tpr, NormShared& sh, int& buf) {
+__device__ __forceinline__ float row_sum(float v, int tpr, NormShared& sh, int& buf) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
-    if (o < tpr)
-#pragma unroll
-      for (int i = 0; i < NVAL; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-  if (tpr <= 32) return;
+    if (o < tpr) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (tpr <= 32) return v;
   const int lane = threadIdx.x & 31;
-  if (lane == 0)
-#pragma unroll
-    for (int i = 0; i < NVAL; ++i) sh.red[buf][i][threadIdx.x >> 5] = v[i];
+  if (lane == 0) sh.red[buf][threadIdx.x >> 5] = v;
   __syncthreads();
+  v = sh.red[buf][lane & (kNormWarps - 1)];
 #pragma unroll
-  for (int i = 0; i < NVAL; ++i) v[i] = sh.red[buf][i][lane & (kNormWarps - 1)];
-#pragma unroll
-  for (int o = kNormWarps / 2; o > 0; o >>= 1)
-#pragma unroll
-    for (int i = 0; i < NVAL; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+  for (int o = kNormWarps / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   buf ^= 1;
+  return v;
 }
-// The same for six sums at once.  A warp's two halves take three of them each
+// Six sums at once.  A warp's two halves take three of them each
 // after the first exchange, so 30 shuffles do what 54 would.
 struct NormShared6 {
   float red[2][6][kNormWarps];
@@ -228,13 +221,12 @@ __global__ void __launch_bounds__(512) norm_fwd(const NormParams p, const int tp
     for (int i = 0; i < NV; ++i) y[i] = raw_get(cur.h[i], f32<TP>(p, kH32));
     float2 k = both(1.f);
     if (p.w_post) {
-      float q[1] = {0.f};
+      float q = 0.f;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) q[0] = dot8(y[i], y[i], q[0]);
-      row_sum(q, tpr, sh, buf);
-      k = both(rsqrtf(fmaf(q[0], invD, p.eps)));
+      for (int i = 0; i < NV; ++i) q = dot8(y[i], y[i], q);
+      k = both(rsqrtf(fmaf(row_sum(q, tpr, sh, buf), invD, p.eps)));
     }
-    float q[1] = {0.f};
+    float q = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = 8 * (i * tpr + t);
@@ -253,11 +245,10 @@ __global__ void __launch_bounds__(512) norm_fwd(const NormParams p, const int tp
 #pragma unroll
       for (int j = 0; j < 4; ++j) y[i].v[j] = lfma(y[i].v[j], sc.v[j], r.v[j]);
       if (p.s && ok) store8(p.s, row * p.D + c, f32<TP>(p, kS32), y[i]);
-      q[0] = dot8(y[i], y[i], q[0]);
+      q = dot8(y[i], y[i], q);
     }
     if (p.w_pre) {
-      row_sum(q, tpr, sh, buf);
-      const float2 ks = both(rsqrtf(fmaf(q[0], invD, p.eps)));
+      const float2 ks = both(rsqrtf(fmaf(row_sum(q, tpr, sh, buf), invD, p.eps)));
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = 8 * (i * tpr + t);
@@ -602,10 +593,10 @@ NormShape norm_shape(int D) {
   return s;
 }
 
-// Blocks: all that 148 SMs hold at once (`regs_threads` threads an SM by their
+// Blocks: all that the SMs hold at once (`sm_threads` threads each by their
 // registers), or one for each of fewer groups of rows.
 int norm_blocks(long long N, const NormShape& s, int sm_threads) {
-  const long long most = 148 * std::max(1, sm_threads / s.threads);
+  const long long most = kSMs * std::max(1, sm_threads / s.threads);
   return (int)std::min<long long>((N + s.slots() - 1) / s.slots(), most);
 }
 constexpr int kFwdThreads = 1024, kBwdThreads = 512, kBwdMost = 1024;

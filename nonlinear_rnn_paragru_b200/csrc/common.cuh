@@ -15,6 +15,8 @@ namespace pararnn {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kChan = 32;  // channels per tile (one warp width)
+// SMs of a B200: the layer operators' shapes and workspaces go by it wherever they are asked for
+constexpr int kSMs = 148;
 
 // ------------------------------------------------------------ arithmetic --
 // 2^x on the MUFU pipe (ftz).  Saturates to +inf / 0.

@@ -655,16 +655,16 @@ int launch_scan(Kern kern, int GL, int threads, int smem, LinParams p, int CL, S
 
 long long tiles_of(int B, int D, int GL) { return (long long)B * ((D + 2 * GL - 1) / (2 * GL)); }
 
-// clusters of 8 on 64-channel tiles would not fill 148 SMs
-bool few_tiles(int B, int D) { return tiles_of(B, D, 32) * kLinMaxCluster <= 148; }
+// clusters of 8 on 64-channel tiles would not fill the SMs
+bool few_tiles(int B, int D) { return tiles_of(B, D, 32) * kLinMaxCluster <= kSMs; }
 
-// CTAs of a cluster: as many as fill one wave of H::R CTAs on each of 148 SMs,
+// CTAs of a cluster: as many as fill one wave of H::R CTAs on each SM,
 // no more than the sequence has rounds of one CTA for.
 template <typename H>
 int cluster_of(int B, int T, int D) {
   const long long tiles = tiles_of(B, D, H::GL);
   int CL = 1;
-  while (CL < kLinMaxCluster && 2 * tiles * CL <= 148 * H::R && T > CL * H::W * H::U::kNG * H::K) CL *= 2;
+  while (CL < kLinMaxCluster && 2 * tiles * CL <= kSMs * H::R && T > CL * H::W * H::U::kNG * H::K) CL *= 2;
   return CL;
 }
 

@@ -707,11 +707,14 @@ int launch_norm_bwd(NormParams p, float* dw_post, float* dscale, float* dw_pre, 
   p.types = canonical_types(p, p.ds, p.dx);
   p.parts = (p.w_post ? kPost : 0) | (p.g ? kGate : 0) | (p.res ? kRes : 0) | (p.scale ? kScale : 0) |
             (p.w_pre ? kPre : 0) | (p.ds ? kDs : 0);
-  // threads that an SM's registers hold: more where fewer parts leave more, and
-  // its shared memory still holds a row ahead (a third with a first norm)
+  // Threads that an SM's registers hold: more where fewer parts leave more, and
+  // its shared memory still holds a row ahead (a third with a first norm).  The
+  // residual pre-norm's kernels have up to 64 registers a thread (1024 threads;
+  // N32768 D1024 fp32 residual 104 us against 114 with 512), the gated norm's up
+  // to 76 (768 threads: N32768 D1024 101 us against 113 with 512, 105 with 640).
   int sm_threads = kBwdThreads, S;
   if (p.D > 256 && p.D <= 4096 && (p.parts == kPartsPre || p.parts == kPartsPost)) {
-    const int more = p.parts == kPartsPre ? kBwdMost : 640;
+    const int more = p.parts == kPartsPre ? kBwdMost : 768;
     bwd_ring(p, s, more, S);
     if (S >= (p.parts == kPartsPost ? 3 : 2)) sm_threads = more;
   }

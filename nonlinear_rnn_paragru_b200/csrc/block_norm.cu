@@ -12,10 +12,12 @@
 // and a thread loads its share of the next row before it works on this one, so
 // that HBM stays busy through the row's two sums.
 //
-// Measured (B200, warm): all parts, fp32 states, the rest bf16: N32768 D1024
-// forward 65.5 us (403 MB: 6.1 TB/s, held by HBM), adjoint 140 us; N8192 D4096
-// adjoint 145 us (671 MB: 4.6 TB/s), held by the latency of a row's phases in the
-// one block that the registers (weights and their sums: 48) leave an SM.
+// Measured (B200, device time, warm): all parts, fp32 states, the rest bf16: N32768
+// D1024 forward 65.5 us (403 MB: 6.1 TB/s, held by HBM), adjoint 139 us; N8192
+// D4096 adjoint 141 us (671 MB: 4.8 TB/s).  The adjoint is held by its instructions
+// (some 88 a channel of a thread, issued in 60% of the cycles) and the latency of a
+// row's phases in the 16 warps that the registers (weights and their sums: 48)
+// leave an SM.  Rows past 4096 channels spill: N4096 D8192 213 us.
 #include <algorithm>
 #include <utility>
 

@@ -17,10 +17,12 @@
 // (16-byte cp.async, S - 1 rounds ahead), which keeps HBM busy through the
 // rounds' barriers without holding registers.
 //
-// Measured (B200, warm): LIN_GRU B8 T4096 D1024 bf16 solve 61 us (268 MB: 4.4
-// TB/s), held by the special-function unit (four a pair of gates) and the
-// rounds' exchanges; its adjoint 93 us (537 MB: 5.8 TB/s) and the LIN_DECAY solve
-// of 65536 steps of 2048 channels in fp32, 344 us (2.15 GB: 6.2 TB/s), by HBM.
+// Measured (B200, device time, warm): LIN_GRU B8 T4096 D1024 bf16 solve 58 us (268
+// MB: 4.6 TB/s).  Nothing is full there (special functions 61% of their rate,
+// issue 48%, HBM 56%): an SM's 12 warps wait for loads and for one another's
+// rounds.  Its adjoint 94 us (537 MB: 5.7 TB/s) and the LIN_DECAY solve of 65536
+// steps of 2048 channels in fp32, 344-370 us (2.15 GB: 5.8-6.2 TB/s), are held by
+// HBM.  A call from Python among others, the GPU under load: 60, 104, 396 us.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -246,15 +248,15 @@ __device__ __forceinline__ void by_marks(unsigned resets, F f) {
 //   kTall    the longest rounds that leave two to four CTAs on an SM.  With fp32
 //            u a round is published before the round before it ends (kAhead), so
 //            its exchange runs behind the next round's arithmetic, at twice the
-//            registers for maps: LIN_DECAY T65536 D2048 344 us against 422,
-//            LIN_GRU B8 T4096 D1024 66 against 70.  With bf16 the registers cost
-//            more CTAs than that gains (61 against 61 at best).
+//            registers for maps: LIN_DECAY T65536 D2048 344-370 us against
+//            416-424, LIN_GRU B8 T4096 D1024 66 against 69.  With bf16 the
+//            registers cost as many CTAs as that gains.
 //   kShort   LIN_GRU with bf16 u: 8 steps, five CTAs, taken where that lets the
-//            cluster grow (300 tiles of 2048 steps: 70 us against 83; 128 tiles
-//            of 4096 steps: 64 against 61)
+//            cluster grow (300 tiles of 2048 steps: 69 us against 80; 128 tiles
+//            of 4096 steps: 62 against 58)
 //   kNarrow  tiles of 16 channels, for problems of so few 64-channel tiles that
-//            clusters of 8 CTAs leave SMs idle (one tile of 16384 steps: 17 us
-//            against 54; 16 tiles of 65536 steps: 169 against 249)
+//            clusters of 8 CTAs leave SMs idle (one tile of 16384 steps: 16 us
+//            against 51; 16 tiles of 65536 steps: 164 against 225)
 enum Variant { kTall, kShort, kNarrow };
 template <int CELL, bool kBF16, int V>
 struct FwdShape {
@@ -608,7 +610,8 @@ __global__ void __launch_bounds__(32 * BwdShape<CELL, kBF16, V>::W, BwdShape<CEL
 }
 
 // One decode step: a thread owns two channels of one row; h_prev may be h_next.
-// A launch and one wave: 2 us for one row of 1024 channels, 6 us for 256 of 4096.
+// A launch: 2 us for one row of 1024 channels; 6.5 us for 256 of 4096, 1.7 waves of
+// blocks.
 template <int CELL, bool kBF16>
 __global__ void __launch_bounds__(256) linrec_step(const LinParams p, const float* h_prev, float* h_next) {
   using Cell = LinCell<CELL>;
